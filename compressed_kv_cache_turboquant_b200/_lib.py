@@ -13,10 +13,10 @@ LIB_PATH = os.path.join(_HERE, "libtq_b200.so")
 
 TQ_OK, TQ_EINVAL, TQ_EUNSUPPORTED, TQ_EALIGN, TQ_ECUDA, TQ_ENOMEM, TQ_EWORKSPACE = range(7)
 TQ_F32, TQ_BF16, TQ_F16 = 0, 1, 2
-TQ_MSE, TQ_PROD, TQ_POLAR = 0, 1, 2
+TQ_MSE, TQ_PROD, TQ_POLAR, TQ_KV8 = 0, 1, 2, 3
 TQ_MAX_DIM = 4096
 TQ_MAX_TOPK = 64
-TQ_STATUS_TIMEOUT, TQ_STATUS_LAYOUT = 1, 2
+TQ_STATUS_TIMEOUT, TQ_STATUS_LAYOUT, TQ_STATUS_RANGE = 1, 2, 4
 TQ_MAX_SHARDS = 64
 TQ_DECODE_STATIC_SCRATCH = 4 * 1024 * 1024
 
@@ -69,6 +69,9 @@ SIGNATURES = {
     "tq_create_polar": (_i, [ctypes.POINTER(_p), _i, _i, _i, _dp]),
     "tq_quant_polar": (_i, [_p, _p, _i, _i64, _i64, _p, _p, _i64, _p]),
     "tq_dequant_polar": (_i, [_p, _p, _p, _i64, _p, _i, _p]),
+    "tq_create_kv8": (_i, [ctypes.POINTER(_p), _i]),
+    "tq_quant_kv8": (_i, [_p, _p, _p, _i, _i64, _i, _i64, _i64, _p, _p, _p, _p, _p, _i64, _p]),
+    "tq_dequant_kv8": (_i, [_p, _i64, _p, _p, _p, _p, _p, _i64, _p, _p, _i, _p]),
     "tq_device_status": (_i, [_p, ctypes.POINTER(_i)]),
     "tq_quant_gather": (_i, [_p, _p, _i, _i64, _i64, _p, _p, _p, _p, _p, _i64, _p]),
     "tq_quant_gather_groups": (_i, [ctypes.POINTER(_p), _i, _p, _i, _i64, _i64, _p, ctypes.POINTER(_p),

@@ -12,8 +12,8 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import (TQ_BF16, TQ_F16, TQ_F32, TQ_MAX_TOPK, TQ_POLAR, TQ_MSE, TQ_PROD, TQ_STATUS_LAYOUT, TQ_STATUS_TIMEOUT, TQError,
-                   check, lib)
+from ._lib import (TQ_BF16, TQ_F16, TQ_F32, TQ_KV8, TQ_MAX_TOPK, TQ_POLAR, TQ_MSE, TQ_PROD, TQ_STATUS_LAYOUT,
+                   TQ_STATUS_RANGE, TQ_STATUS_TIMEOUT, TQError, check, lib)
 
 __all__ = [
     "TQ_MSE", "TQ_PROD", "TQ_F32", "TQ_BF16", "TQ_F16", "TQ_MAX_TOPK", "TQ_STATUS_TIMEOUT", "TQ_STATUS_LAYOUT", "TQError", "Handle", "code_words", "sign_words",
@@ -24,7 +24,7 @@ __all__ = [
     "tq_attn_decode_partial", "tq_attn_decode_partial_workspace", "tq_attn_merge", "tq_topk_merge",
     "tq_quant_paged", "tq_attn_decode_paged", "tq_quant_gather_groups", "tq_attn_prefill",
     "tq_attn_prefill_workspace", "TQ_POLAR", "tq_polar_codebook", "tq_create_polar", "tq_quant_polar",
-    "tq_dequant_polar",
+    "tq_dequant_polar", "TQ_KV8", "TQ_STATUS_RANGE", "tq_create_kv8", "tq_quant_kv8", "tq_dequant_kv8",
 ]
 
 
@@ -91,12 +91,14 @@ class Handle:
     def __init__(self, ptr: int, d: int, b: int, variant: int, bh: int = 0):
         self.ptr = ptr
         self.d, self.b, self.variant, self.bh = d, b, variant, bh
-        self.bm = b if variant in (TQ_MSE, TQ_POLAR) else b - 1
+        self.bm = b - 1 if variant == TQ_PROD else b
 
     @property
     def words(self) -> int:
         if self.variant == TQ_POLAR:
             return code_words(self.b, self.d // 2) + code_words(self.bh, self.d // 2 - 1)
+        if self.variant == TQ_KV8:
+            return self.d // 4
         return code_words(self.bm, self.d)
 
     def close(self):
@@ -307,6 +309,116 @@ def tq_attn_prefill(hk: Handle, hv: Handle, q: torch.Tensor, Hkv: int, T: int, k
         hk.ptr, hv.ptr, _ptr(q), _dtype_code(q), B, nq, Hq, Hkv, T, kv_stride, _ptr(kcodes), _ptr(ksigns),
         _ptr(knorms), _ptr(krnorms), _ptr(vcodes), _ptr(vnorms), float(scale), _ptr(out), _ptr(workspace),
         workspace.numel(), _stream(stream)))
+
+
+# ---- the 8-bit cache
+
+_DTYPES = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
+
+
+def _dtype3(t: torch.Tensor) -> int:
+    """The type code of a call that also takes float16 activations."""
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"unsupported dtype {t.dtype}") from None
+
+
+def _stream_on(stream, t: torch.Tensor) -> int:
+    """The given stream, or the current one of the device that holds t."""
+    if stream is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _same_device(*tensors) -> None:
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("expected a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor (this library has no CPU path)")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+
+
+def _token_rows(t: torch.Tensor, name: str, heads: int, d: int) -> int:
+    """Checks [tokens][heads][d] with whole heads side by side; returns the
+    elements from one token to the next (a slice of a fused projection has more
+    than heads d of them)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name}: expected [tokens][{heads}][{d}], got {tuple(t.shape)}")
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must lie side by side")
+    return t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def _cache_rows(h: Handle, kcodes, kscales, vcodes, vscales) -> int:
+    """Checks the four cache arrays (the values may be None); returns their rows."""
+    pairs = [(kcodes, kscales)]
+    if vcodes is not None or vscales is not None:
+        pairs.append((vcodes, vscales))
+    for codes, scales in pairs:
+        if codes is None or codes.dtype != torch.int8 or codes.dim() != 2 or codes.shape != (kcodes.shape[0], h.d):
+            raise ValueError(f"codes: expected int8 [rows][{h.d}], the same rows for keys and values")
+        if scales is None or scales.dtype != torch.float32 or scales.shape != kcodes.shape[:1]:
+            raise ValueError("scales: expected float32 [rows], as many as the codes")
+    return kcodes.shape[0]
+
+
+def tq_create_kv8(d: int) -> Handle:
+    """A handle of the 8-bit cache for heads of dimension d."""
+    h = ctypes.c_void_p()
+    check("tq_create_kv8", lib.tq_create_kv8(ctypes.byref(h), d))
+    return Handle(h.value, d, 8, TQ_KV8)
+
+
+def tq_quant_kv8(h: Handle, k: torch.Tensor, v, slots: torch.Tensor, kcodes: torch.Tensor, kscales: torch.Tensor,
+                 vcodes=None, vscales=None, stream=None) -> None:
+    """Quantize the keys and values of n tokens, [n][Hkv][d] each (a token
+    stride is allowed; v may be None), into cache rows slots [n][Hkv] (int64,
+    negative: left out)."""
+    _same_device(k, v, slots, kcodes, kscales, vcodes, vscales)
+    if k.dim() != 3:
+        raise ValueError(f"k: expected [tokens][heads][d], got {tuple(k.shape)}")
+    n, Hkv = k.shape[0], k.shape[1]
+    ks = _token_rows(k, "k", Hkv, h.d)
+    vs = 0 if v is None else _token_rows(v, "v", Hkv, h.d)
+    if v is not None and (v.shape[0] != n or v.dtype != k.dtype or vcodes is None or vscales is None):
+        raise ValueError("v: expected as many tokens as k, of its type, and arrays for their codes and scales")
+    if slots.dtype != torch.int64 or slots.numel() != n * Hkv:
+        raise ValueError(f"slots: expected int64 [{n}][{Hkv}], got {slots.dtype} {tuple(slots.shape)}")
+    rows = _cache_rows(h, kcodes, kscales, vcodes, vscales)
+    if n == 0 or Hkv == 0:
+        return
+    check("tq_quant_kv8", lib.tq_quant_kv8(h.ptr, k.data_ptr(), None if v is None else v.data_ptr(), _dtype3(k), n, Hkv,
+                                           ks, vs, _ptr(slots), _ptr(kcodes), _ptr(kscales), _ptr(vcodes),
+                                           _ptr(vscales), rows, _stream_on(stream, k)))
+
+
+def tq_dequant_kv8(h: Handle, slots: torch.Tensor, kcodes: torch.Tensor, kscales: torch.Tensor, vcodes, vscales,
+                   k: torch.Tensor, v=None, stream=None) -> None:
+    """Read cache rows slots [n] (int64; outside the cache: zeros) back into k
+    and v, [n][d] each (v may be None)."""
+    _same_device(slots, kcodes, kscales, vcodes, vscales, k, v)
+    n = slots.numel()
+    if slots.dtype != torch.int64:
+        raise ValueError(f"slots: expected int64, got {slots.dtype}")
+    for t in (k,) if v is None else (k, v):
+        if t.numel() != n * h.d or t.shape[-1] != h.d or t.dtype != k.dtype:
+            raise ValueError(f"outputs: expected [{n}][{h.d}] of one type, got {tuple(t.shape)} {t.dtype}")
+    if v is not None and (vcodes is None or vscales is None):
+        raise ValueError("v: needs the values' codes and scales")
+    rows = _cache_rows(h, kcodes, kscales, vcodes, vscales)
+    if n == 0:
+        return
+    check("tq_dequant_kv8", lib.tq_dequant_kv8(h.ptr, n, _ptr(slots), _ptr(kcodes), _ptr(kscales), _ptr(vcodes),
+                                               _ptr(vscales), rows, _ptr(k), _ptr(v), _dtype3(k),
+                                               _stream_on(stream, k)))
 
 
 def tq_device_status(h: Handle) -> int:

@@ -54,6 +54,18 @@ int ensure_dyn_smem(const void* kernel, int bytes) {
   return (int)e;
 }
 
+DeviceGuard::DeviceGuard(int device) {
+  int cur = 0;
+  error = (int)cudaGetDevice(&cur);
+  if (error || cur == device) return;
+  error = (int)cudaSetDevice(device);
+  if (!error) prev = cur;
+}
+
+DeviceGuard::~DeviceGuard() {
+  if (prev >= 0) cudaSetDevice(prev);
+}
+
 static int cuda_error(const char* where, int e) {
   return set_error(TQ_ECUDA, "%s: %s", where, cudaGetErrorString((cudaError_t)e));
 }
@@ -572,6 +584,7 @@ extern "C" int tq_dequant_mse(tq_handle h, const uint32_t* codes, const float* n
   TQ_TRACE("tq_dequant_mse");
   if (!h) return set_error(TQ_EINVAL, "tq_dequant_mse: NULL handle");
   if (h->variant == TQ_POLAR) return set_error(TQ_EINVAL, "tq_dequant_mse: a TQ_POLAR handle (use tq_dequant_polar)");
+  if (h->variant == TQ_KV8) return set_error(TQ_EINVAL, "tq_dequant_mse: a TQ_KV8 handle (use tq_dequant_kv8)");
   if (N < 0) return set_error(TQ_EINVAL, "tq_dequant_mse: N < 0");
   if (out_dtype != TQ_F32 && out_dtype != TQ_BF16)
     return set_error(TQ_EUNSUPPORTED, "tq_dequant_mse: out_dtype %d", out_dtype);
@@ -602,6 +615,7 @@ extern "C" int tq_ip_scores(tq_handle h, const float* q, int64_t nq, const uint3
   TQ_TRACE("tq_ip_scores");
   if (!h) return set_error(TQ_EINVAL, "tq_ip_scores: NULL handle");
   if (h->variant == TQ_POLAR) return set_error(TQ_EINVAL, "tq_ip_scores: a TQ_POLAR handle");
+  if (h->variant == TQ_KV8) return set_error(TQ_EINVAL, "tq_ip_scores: a TQ_KV8 handle");
   if (nq < 0 || N < 0) return set_error(TQ_EINVAL, "tq_ip_scores: negative size");
   if (topk < 0 || topk > TQ_MAX_TOPK || (topk > 0 && topk > N && N > 0))
     return set_error(TQ_EINVAL, "tq_ip_scores: topk %d (need 0..min(N, %d))", topk, TQ_MAX_TOPK);
@@ -756,6 +770,7 @@ extern "C" int tq_quant_gather(tq_handle h, const void* x, int dtype, int64_t N,
   TQ_TRACE("tq_quant_gather");
   if (!h) return set_error(TQ_EINVAL, "tq_quant_gather: NULL handle");
   if (h->variant == TQ_POLAR) return set_error(TQ_EINVAL, "tq_quant_gather: a TQ_POLAR handle");
+  if (h->variant == TQ_KV8) return set_error(TQ_EINVAL, "tq_quant_gather: a TQ_KV8 handle");
   if (N < 0) return set_error(TQ_EINVAL, "tq_quant_gather: N < 0");
   if (dtype != TQ_F32 && dtype != TQ_BF16) return set_error(TQ_EUNSUPPORTED, "tq_quant_gather: dtype %d", dtype);
   if (x_stride < 1 || out_stride < 1) return set_error(TQ_EINVAL, "tq_quant_gather: stride < 1");
@@ -799,6 +814,7 @@ extern "C" int tq_quant_gather_groups(const tq_handle* h, int ngroups, const voi
   for (int g = 0; g < ngroups; ++g) {
     if (!h[g]) return set_error(TQ_EINVAL, "%s: NULL handle", fn);
     if (h[g]->variant == TQ_POLAR) return set_error(TQ_EINVAL, "%s: a TQ_POLAR handle", fn);
+    if (h[g]->variant == TQ_KV8) return set_error(TQ_EINVAL, "%s: a TQ_KV8 handle", fn);
     if (h[g]->d > 256) return set_error(TQ_EUNSUPPORTED, "%s: d = %d (need <= 256)", fn, h[g]->d);
     const bool prod = h[g]->variant == TQ_PROD;
     if (!codes[g] || !norms[g] || (prod && (!signs || !rnorms || !signs[g] || !rnorms[g])))

@@ -1,0 +1,374 @@
+// The 8-bit paged K/V cache: rows quantized as they are written, and read back.
+//
+// The cache of the newest and the drafted tokens, which come and go faster
+// than a rotation and a codebook pay for (ttakun.com/news/45354,
+// 新旧量化方案深度权衡矩阵: each token is compressed as it arrives; tmdm.cn, 实测数据:
+// only the KV store and load change).  A row (one token of one kv-head) is
+//   s = max_j |x_j| / 127 (float32),  c_j = x_j / s rounded to the nearest
+//   integer (ties to even), kept in [-127, 127],
+// and stands for c_j s.  Codes are exactly those of the quotient by the stored
+// s: a first guess x (1/s) can only miss by one next to a tie, and the exact
+// remainder x - c s (one fused multiply-add: x and c s are multiples of half
+// an ulp of s, and their difference is at most about s / 2, so it has 24 bits)
+// decides there.  A row that holds an infinity or a NaN has no such codes: it
+// gets s = NaN and codes 0, so that what reads it gets NaN in that row alone.
+//
+// Both directions are bound by HBM: d e + d + 4 bytes a row and tensor, plus 8
+// of the slot list (e: bytes of an element of x).  Eight elements a thread make
+// every load of 16-bit inputs, and every store of 16-bit outputs, a whole
+// 16-byte unit of neighbouring lanes; four rows a thread keep their loads in
+// flight together.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <initializer_list>
+#include <new>
+
+#include "sm100_common.cuh"
+#include "tq_internal.h"
+
+namespace tqi {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 256;
+constexpr int kRowsPerThread = 4;
+
+struct Kv8Args {
+  const void* x[2];        // write: keys, values; read: unused
+  void* out[2];            // read: keys, values
+  int8_t* codes[2];
+  float* scales[2];
+  const int64_t* slots;
+  int64_t x_stride[2];     // elements from one token to the next
+  int64_t N;               // rows: tokens x heads
+  int64_t rows;            // rows of the cache
+  int Hkv, d;
+  int* status;
+};
+
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it leaves the nearest integer in the low bits
+
+// the code of x for scale s > 0: x / s to the nearest integer, ties to even
+__device__ __forceinline__ int exact_code(float x, float s, float guess) {
+  float q = fminf(fmaxf(guess, -127.f), 127.f);
+  const float r = fmaf(-q, s, x);
+  const float twice = fabsf(r) + fabsf(r);
+  if (twice > s || (twice == s && ((int)q & 1))) q += r > 0.f ? 1.f : -1.f;
+  return (int)fminf(fmaxf(q, -127.f), 127.f);
+}
+
+// lanes: threads of a row (a power of two >= d / 8), so that a row never
+// crosses a warp; the lanes past d / 8 only take part in the shuffles
+template <typename T>
+__global__ void __launch_bounds__(kThreads) kv8_write_kernel(Kv8Args a, int lanes) {
+  const int which = blockIdx.y;
+  const int sub = threadIdx.x & (lanes - 1);
+  const int groups = kThreads / lanes;
+  const bool on = sub * 8 < a.d;
+  const T* x = static_cast<const T*>(a.x[which]);
+  const int64_t r0 = (int64_t)blockIdx.x * (groups * kRowsPerThread) + threadIdx.x / lanes;
+  float v[kRowsPerThread][8];
+  int64_t slot[kRowsPerThread];
+#pragma unroll
+  for (int i = 0; i < kRowsPerThread; ++i) {
+    const int64_t n = r0 + (int64_t)i * groups;
+    slot[i] = -1;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+    if (n < a.N) {
+      slot[i] = __ldg(a.slots + n);
+      const uint32_t t = (uint32_t)n / (uint32_t)a.Hkv, h = (uint32_t)n - t * (uint32_t)a.Hkv;
+      if (on) load8(x + (int64_t)t * a.x_stride[which] + (int64_t)h * a.d + sub * 8, v[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerThread; ++i) {
+    // |x| ordered by its bits, so that an infinity or a NaN comes out on top
+    uint32_t mx = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mx = max(mx, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+    for (int m = lanes >> 1; m; m >>= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, m));
+    const bool finite = mx < 0x7F800000u;
+    const float s = finite ? __fdiv_rn(__uint_as_float(mx), 127.f) : __uint_as_float(0x7FC00000u);
+    uint32_t c[8];
+    if (!finite || s == 0.f) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = 0;
+    } else if (s >= 0x1p-80f) {
+      const float inv = __frcp_rn(s);
+      bool near = false;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float g = fmaf(v[i][e], inv, kMagic);
+        c[e] = __float_as_uint(g);
+        const float r = fmaf(-(g - kMagic), s, v[i][e]);
+        // off by more than just under half a step: a tie, or the wrong side of one
+        near |= fabsf(r) > 0.4999f * s;
+      }
+      if (near) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = (uint32_t)exact_code(v[i][e], s, rintf(v[i][e] * inv));
+      }
+    } else {
+      // 1/s would leave float32's range: the guess from both scaled up
+      const float inv = __frcp_rn(s * 0x1p100f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = (uint32_t)exact_code(v[i][e], s, rintf(v[i][e] * 0x1p100f * inv));
+    }
+    if (slot[i] >= 0 && slot[i] < a.rows) {
+      if (on) {
+        uint2 w;
+        w.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        w.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+        *reinterpret_cast<uint2*>(a.codes[which] + slot[i] * a.d + sub * 8) = w;
+      }
+      if (sub == 0) a.scales[which][slot[i]] = s;
+    } else if (slot[i] >= a.rows && sub == 0) {
+      atomicOr(a.status, kStatusRange);
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) kv8_read_kernel(Kv8Args a, int lanes) {
+  const int which = blockIdx.y;
+  const int sub = threadIdx.x & (lanes - 1);
+  const int groups = kThreads / lanes;
+  if (sub * 8 >= a.d) return;
+  T* out = static_cast<T*>(a.out[which]);
+  const int64_t r0 = (int64_t)blockIdx.x * (groups * kRowsPerThread) + threadIdx.x / lanes;
+  int64_t slot[kRowsPerThread];
+  uint2 w[kRowsPerThread];
+  float s[kRowsPerThread];
+#pragma unroll
+  for (int i = 0; i < kRowsPerThread; ++i) {
+    const int64_t n = r0 + (int64_t)i * groups;
+    slot[i] = n < a.N ? __ldg(a.slots + n) : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerThread; ++i) {
+    w[i] = make_uint2(0u, 0u);
+    s[i] = 0.f;
+    if (slot[i] >= 0 && slot[i] < a.rows) {
+      w[i] = __ldg(reinterpret_cast<const uint2*>(a.codes[which] + slot[i] * a.d + sub * 8));
+      s[i] = __ldg(a.scales[which] + slot[i]);
+    } else if (slot[i] >= a.rows && sub == 0) {
+      atomicOr(a.status, kStatusRange);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerThread; ++i) {
+    const int64_t n = r0 + (int64_t)i * groups;
+    if (n >= a.N) continue;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t word = e < 4 ? w[i].x : w[i].y;
+      v[e] = (float)(int8_t)(word >> (8 * (e & 3))) * s[i];
+    }
+    store8(out + n * a.d + sub * 8, v);
+  }
+}
+
+int lanes_of(int d) {
+  int l = 2;
+  while (l * 8 < d) l *= 2;
+  return l;
+}
+
+}  // namespace
+
+int launch_kv8_write(const tq_ctx* h, const void* k, const void* v, int dtype, int64_t n, int Hkv, int64_t k_stride,
+                     int64_t v_stride, const int64_t* slots, int8_t* kcodes, float* kscales, int8_t* vcodes,
+                     float* vscales, int64_t rows, void* stream) {
+  Kv8Args a{};
+  a.x[0] = k, a.x[1] = v;
+  a.codes[0] = kcodes, a.codes[1] = vcodes;
+  a.scales[0] = kscales, a.scales[1] = vscales;
+  a.slots = slots;
+  a.x_stride[0] = k_stride, a.x_stride[1] = v_stride;
+  a.N = n * Hkv, a.rows = rows, a.Hkv = Hkv, a.d = h->d, a.status = h->dev.status;
+  const int lanes = lanes_of(h->d), per = kThreads / lanes * kRowsPerThread;
+  const dim3 grid((unsigned)((a.N + per - 1) / per), v ? 2 : 1);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == TQ_F32)
+    kv8_write_kernel<float><<<grid, kThreads, 0, st>>>(a, lanes);
+  else if (dtype == TQ_BF16)
+    kv8_write_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, lanes);
+  else
+    kv8_write_kernel<__half><<<grid, kThreads, 0, st>>>(a, lanes);
+  return (int)cudaGetLastError();
+}
+
+int launch_kv8_read(const tq_ctx* h, int64_t N, const int64_t* slots, const int8_t* kcodes, const float* kscales,
+                    const int8_t* vcodes, const float* vscales, int64_t rows, void* k, void* v, int dtype,
+                    void* stream) {
+  Kv8Args a{};
+  a.out[0] = k, a.out[1] = v;
+  a.codes[0] = const_cast<int8_t*>(kcodes), a.codes[1] = const_cast<int8_t*>(vcodes);
+  a.scales[0] = const_cast<float*>(kscales), a.scales[1] = const_cast<float*>(vscales);
+  a.slots = slots;
+  a.N = N, a.rows = rows, a.Hkv = 1, a.d = h->d, a.status = h->dev.status;
+  const int lanes = lanes_of(h->d), per = kThreads / lanes * kRowsPerThread;
+  const dim3 grid((unsigned)((a.N + per - 1) / per), v ? 2 : 1);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == TQ_F32)
+    kv8_read_kernel<float><<<grid, kThreads, 0, st>>>(a, lanes);
+  else if (dtype == TQ_BF16)
+    kv8_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, lanes);
+  else
+    kv8_read_kernel<__half><<<grid, kThreads, 0, st>>>(a, lanes);
+  return (int)cudaGetLastError();
+}
+
+}  // namespace tqi
+
+using namespace tqi;
+
+namespace {
+
+// the checks of the cache arrays that both directions share
+int check_kv8(const char* fn, int64_t rows, const void* kcodes, const void* kscales, const void* vcodes,
+              const void* vscales, bool values) {
+  if (rows < 0) return set_error(TQ_EINVAL, "%s: rows < 0", fn);
+  if (!kcodes || !kscales || (values && (!vcodes || !vscales))) return set_error(TQ_EINVAL, "%s: NULL pointer", fn);
+  return TQ_OK;
+}
+
+int check_aligned(const char* fn, std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) & 15u)
+      return set_error(TQ_EALIGN, "%s: a device pointer is not 16-byte aligned", fn);
+  return TQ_OK;
+}
+
+}  // namespace
+
+extern "C" int tq_create_kv8(tq_handle* out, int d) {
+  TQ_TRACE("tq_create_kv8");
+  if (!out) return set_error(TQ_EINVAL, "tq_create_kv8: NULL handle");
+  *out = nullptr;
+  if (d < 16 || d > 256 || d % 16 != 0)
+    return set_error(TQ_EUNSUPPORTED, "tq_create_kv8: d = %d (need 16 <= d <= 256, d %% 16 == 0)", d);
+  tq_ctx* h = new (std::nothrow) tq_ctx();
+  if (!h) return set_error(TQ_ENOMEM, "tq_create_kv8: out of host memory");
+  h->d = d, h->b = 8, h->bm = 8, h->variant = TQ_KV8;
+  cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
+  if (e == cudaSuccess) {
+    h->block_bytes = 256;
+    e = cudaMalloc(&h->block, h->block_bytes);
+    if (e == cudaSuccess) e = cudaMemset(h->block, 0, h->block_bytes);
+    h->dev.status = static_cast<int*>(h->block);
+  }
+  if (e != cudaSuccess) {
+    if (h->block) cudaFree(h->block);
+    delete h;
+    return set_error(e == cudaErrorMemoryAllocation ? TQ_ENOMEM : TQ_ECUDA, "tq_create_kv8: %s", cudaGetErrorString(e));
+  }
+  *out = h;
+  return clear_error();
+}
+
+extern "C" int tq_quant_kv8(tq_handle h, const void* k, const void* v, int dtype, int64_t n, int Hkv,
+                            int64_t k_stride, int64_t v_stride, const int64_t* slots, int8_t* kcodes, float* kscales,
+                            int8_t* vcodes, float* vscales, int64_t rows, void* stream) {
+  TQ_TRACE("tq_quant_kv8");
+  const char* fn = "tq_quant_kv8";
+  if (!h) return set_error(TQ_EINVAL, "%s: NULL handle", fn);
+  if (h->variant != TQ_KV8) return set_error(TQ_EINVAL, "%s: need a TQ_KV8 handle", fn);
+  if (dtype != TQ_F32 && dtype != TQ_BF16 && dtype != TQ_F16) return set_error(TQ_EUNSUPPORTED, "%s: dtype %d", fn, dtype);
+  if (n < 0 || Hkv < 1) return set_error(TQ_EINVAL, "%s: n = %lld, Hkv = %d", fn, (long long)n, Hkv);
+  if (n > INT32_MAX / Hkv) return set_error(TQ_EUNSUPPORTED, "%s: more than 2^31 - 1 rows", fn);
+  const int unit = dtype == TQ_F32 ? 4 : 8;  // elements in 16 bytes
+  for (const int64_t s : {k_stride, v ? v_stride : k_stride})
+    if (n > 1 && (s < (int64_t)Hkv * h->d || s % unit != 0))
+      return set_error(TQ_EINVAL, "%s: stride %lld (need >= Hkv d and a multiple of 16 bytes)", fn, (long long)s);
+  if (n == 0) return clear_error();
+  if (!k || !slots) return set_error(TQ_EINVAL, "%s: NULL pointer", fn);
+  int rc = check_kv8(fn, rows, kcodes, kscales, vcodes, vscales, v != nullptr);
+  if (!rc) rc = check_aligned(fn, {k, v, slots, kcodes, kscales, vcodes, vscales});
+  if (rc) return rc;
+  DeviceGuard guard(h->device);
+  const int e = guard.error ? guard.error
+                            : launch_kv8_write(h, k, v, dtype, n, Hkv, k_stride, v_stride, slots, kcodes, kscales,
+                                               vcodes, vscales, rows, stream);
+  return e ? set_error(TQ_ECUDA, "%s: %s", fn, cudaGetErrorString((cudaError_t)e)) : clear_error();
+}
+
+extern "C" int tq_dequant_kv8(tq_handle h, int64_t n, const int64_t* slots, const int8_t* kcodes,
+                              const float* kscales, const int8_t* vcodes, const float* vscales, int64_t rows, void* k,
+                              void* v, int out_dtype, void* stream) {
+  TQ_TRACE("tq_dequant_kv8");
+  const char* fn = "tq_dequant_kv8";
+  if (!h) return set_error(TQ_EINVAL, "%s: NULL handle", fn);
+  if (h->variant != TQ_KV8) return set_error(TQ_EINVAL, "%s: need a TQ_KV8 handle", fn);
+  if (out_dtype != TQ_F32 && out_dtype != TQ_BF16 && out_dtype != TQ_F16)
+    return set_error(TQ_EUNSUPPORTED, "%s: out_dtype %d", fn, out_dtype);
+  if (n < 0) return set_error(TQ_EINVAL, "%s: n < 0", fn);
+  if (n > INT32_MAX) return set_error(TQ_EUNSUPPORTED, "%s: more than 2^31 - 1 rows", fn);
+  if (n == 0) return clear_error();
+  if (!k || !slots) return set_error(TQ_EINVAL, "%s: NULL pointer", fn);
+  int rc = check_kv8(fn, rows, kcodes, kscales, vcodes, vscales, v != nullptr);
+  if (!rc) rc = check_aligned(fn, {k, v, slots, kcodes, kscales, vcodes, vscales});
+  if (rc) return rc;
+  DeviceGuard guard(h->device);
+  const int e = guard.error ? guard.error
+                            : launch_kv8_read(h, n, slots, kcodes, kscales, vcodes, vscales, rows, k, v, out_dtype,
+                                              stream);
+  return e ? set_error(TQ_ECUDA, "%s: %s", fn, cudaGetErrorString((cudaError_t)e)) : clear_error();
+}

@@ -131,6 +131,17 @@ struct tq_ctx {
 
 namespace tqi {
 
+// The handle's device as the current one for the length of a call, and the
+// caller's again after it.
+struct DeviceGuard {
+  int prev = -1;
+  int error = 0;
+  explicit DeviceGuard(int device);
+  ~DeviceGuard();
+  DeviceGuard(const DeviceGuard&) = delete;
+  DeviceGuard& operator=(const DeviceGuard&) = delete;
+};
+
 // A paged K/V cache (page > 0): token t of (batch, kv-head) bh is row
 // block_table[bh * max_pages + t / page] * page + t % page of every array;
 // page == 0 is the dense layout (row bh * kv_stride + t).  rn16: the residual
@@ -252,6 +263,13 @@ int launch_prefill(const tq_ctx* hk, const tq_ctx* hv, const float* qrot, const 
                    int Hkv, int64_t T, int64_t kv_stride, const uint32_t* kcodes, const uint32_t* ksigns,
                    const float* knorms, const float* krnorms, const uint32_t* vcodes, const float* vnorms, float scale,
                    float* partials, float* out, void* stream);
+// the 8-bit cache (a TQ_KV8 handle): n tokens of Hkv heads into rows `slots`, and rows read back
+int launch_kv8_write(const tq_ctx* h, const void* k, const void* v, int dtype, int64_t n, int Hkv, int64_t k_stride,
+                     int64_t v_stride, const int64_t* slots, int8_t* kcodes, float* kscales, int8_t* vcodes,
+                     float* vscales, int64_t rows, void* stream);
+int launch_kv8_read(const tq_ctx* h, int64_t N, const int64_t* slots, const int8_t* kcodes, const float* kscales,
+                    const int8_t* vcodes, const float* vscales, int64_t rows, void* k, void* v, int dtype,
+                    void* stream);
 // decode attention through whichever kernel fits; workspace layout owned here.
 // partial_out: write the (acc[d] in the rotated value frame, m, l) record of
 // every (batch, q-head) to out [B*Hq][d + 2] instead of the normalised output

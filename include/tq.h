@@ -73,7 +73,8 @@ extern "C" {
 /* element types */
 #define TQ_F32 0
 #define TQ_BF16 1
-#define TQ_F16 2  /* storage of residual norms only (tq_quant_paged, tq_attn_decode_paged) */
+#define TQ_F16 2  /* storage of residual norms (tq_quant_paged, tq_attn_decode_paged); inputs and outputs of the
+                     8-bit cache and of tq_attn_prompt, tq_attn_tree */
 
 /* variants */
 #define TQ_MSE 0  /* TurboQuant_mse: b bits per coordinate */
@@ -454,6 +455,66 @@ TQ_API int tq_attn_decode_paged(tq_handle hk, tq_handle hv, const void* q, int q
                                 const void* krnorms, int rn_dtype, const uint32_t* vcodes, const float* vnorms,
                                 float scale, float* out, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- an 8-bit paged cache */
+
+/*
+ * The 8-bit cache holds tokens that are too new or too short-lived for a
+ * rotation and a codebook (the newest window, drafted tokens, layers kept at
+ * higher precision) beside a TurboQuant cache, in the same rows and pages
+ * ([ttakun, "新旧量化方案深度权衡矩阵"]: each token is compressed as it arrives;
+ * [tmdm, "实测数据"]: only the KV store and load change; the 8-bit form itself is
+ * not on the pages).  A row (one token of one kv-head) x is kept as
+ *   s = max_j |x_j| / 127 (float32),  c_j = x_j / s rounded to the nearest
+ *   integer, ties to even, in [-127, 127] (int8)
+ * and stands for c_j s.  s = 0 gives codes 0.  A row that holds an infinity or
+ * a NaN gets s = NaN and codes 0.
+ *   codes   [rows][d] int8;  scales [rows] float32
+ */
+#define TQ_KV8 3
+
+/*
+ * tq_create_kv8 -- a handle of the 8-bit cache (variant TQ_KV8): d and the
+ * status word, no rotation.
+ *   d   head dimension, 16..256 with d % 16 == 0
+ * Allocates 256 bytes on the current device and synchronises.
+ * Errors: TQ_EINVAL, TQ_EUNSUPPORTED, TQ_ENOMEM, TQ_ECUDA.
+ */
+TQ_API int tq_create_kv8(tq_handle* h, int d);
+
+/*
+ * tq_quant_kv8 -- quantize-on-write: the keys and values of n tokens into rows
+ * of the cache, in one launch.
+ *   k, v      dev in, [n][Hkv][d] of `dtype` (TQ_F32, TQ_BF16 or TQ_F16): head h
+ *             of token t at k + t*k_stride + h*d elements (strides a multiple of
+ *             16 bytes and >= Hkv d; not looked at for n <= 1); v NULL: keys only
+ *   slots     dev in, [n][Hkv] int64: the cache row of each (token, head), for
+ *             keys and values alike; a negative slot leaves that vector out
+ *             (padding), one >= rows is left out and sets TQ_STATUS_RANGE; two
+ *             vectors of one call must not share a row
+ *   kcodes, kscales, vcodes, vscales   dev out, the cache arrays (`rows` rows);
+ *             rows that no slot names keep their contents
+ * n * Hkv < 2^31 (TQ_EUNSUPPORTED otherwise).
+ * Errors: TQ_EINVAL, TQ_EUNSUPPORTED, TQ_EALIGN, TQ_ECUDA.
+ */
+TQ_API int tq_quant_kv8(tq_handle h, const void* k, const void* v, int dtype, int64_t n, int Hkv, int64_t k_stride,
+                        int64_t v_stride, const int64_t* slots, int8_t* kcodes, float* kscales, int8_t* vcodes,
+                        float* vscales, int64_t rows, void* stream);
+
+/*
+ * tq_dequant_kv8 -- read rows of the cache back: k_i = c s of row slots[i], and
+ * v_i likewise (for instance accepted tokens on their way into a TurboQuant
+ * cache through tq_quant_paged).
+ *   slots     dev in, [n] int64; a negative slot gives a row of zeros, one >=
+ *             rows too, and sets TQ_STATUS_RANGE
+ *   k, v      dev out, [n][d] of out_dtype (TQ_F32, TQ_BF16 or TQ_F16), each value
+ *             rounded once; v NULL: keys only (vcodes, vscales may be NULL)
+ * n < 2^31 (TQ_EUNSUPPORTED otherwise).
+ * Errors: TQ_EINVAL, TQ_EUNSUPPORTED, TQ_EALIGN, TQ_ECUDA.
+ */
+TQ_API int tq_dequant_kv8(tq_handle h, int64_t n, const int64_t* slots, const int8_t* kcodes, const float* kscales,
+                          const int8_t* vcodes, const float* vscales, int64_t rows, void* k, void* v, int out_dtype,
+                          void* stream);
+
 /* ---------------------------------------------------------------- channel groups */
 
 /*
@@ -595,11 +656,14 @@ TQ_API int tq_dequant_polar(tq_handle h, const uint32_t* codes, const float* nor
  * returned early; its outputs for that call are incomplete.  Bit 1
  * (TQ_STATUS_LAYOUT): a decode or logits kernel built for the shared-memory
  * address that tq_create measured found its dynamic shared window elsewhere
- * and returned without writing its outputs.
+ * and returned without writing its outputs.  Bit 2 (TQ_STATUS_RANGE): a call
+ * over the 8-bit cache met a slot, a page id or a length that lies outside its
+ * array and left that place out.
  * Errors: TQ_EINVAL, TQ_ECUDA.
  */
 #define TQ_STATUS_TIMEOUT 1
 #define TQ_STATUS_LAYOUT 2
+#define TQ_STATUS_RANGE 4
 TQ_API int tq_device_status(tq_handle h, int* status);
 
 /* tq_last_error -- message of the last failing call on this thread ("" if none). */
