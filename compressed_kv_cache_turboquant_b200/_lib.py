@@ -18,6 +18,7 @@ TQ_MAX_DIM = 4096
 TQ_MAX_TOPK = 64
 TQ_STATUS_TIMEOUT, TQ_STATUS_LAYOUT, TQ_STATUS_RANGE = 1, 2, 4
 TQ_MAX_SHARDS = 64
+TQ_MAX_SEQS, TQ_MAX_DRAFT = 4096, 256
 TQ_DECODE_STATIC_SCRATCH = 4 * 1024 * 1024
 
 if not os.path.exists(LIB_PATH):
@@ -72,6 +73,11 @@ SIGNATURES = {
     "tq_create_kv8": (_i, [ctypes.POINTER(_p), _i]),
     "tq_quant_kv8": (_i, [_p, _p, _p, _i, _i64, _i, _i64, _i64, _p, _p, _p, _p, _p, _i64, _p]),
     "tq_dequant_kv8": (_i, [_p, _i64, _p, _p, _p, _p, _p, _i64, _p, _p, _i, _p]),
+    "tq_attn_prompt": (_i, [_p, _p, _p, _p, _i, _p, _i, _i64, _i, _i, _i64, _i64, _i64, _f, _p, _p, _p, _sz, _p]),
+    "tq_attn_prompt_workspace": (_sz, [_p, _i, _i64, _i, _i]),
+    "tq_attn_tree": (_i, [_p, _p, _i, _i64, _i, _i, _i, _i, _p, _p, _p, _p, _i, _i, _p, _p, _p, _p, _i64, _f, _p, _p, _p,
+                          _sz, _p]),
+    "tq_attn_tree_workspace": (_sz, [_p, _i, _i, _i, _i]),
     "tq_device_status": (_i, [_p, ctypes.POINTER(_i)]),
     "tq_quant_gather": (_i, [_p, _p, _i, _i64, _i64, _p, _p, _p, _p, _p, _i64, _p]),
     "tq_quant_gather_groups": (_i, [ctypes.POINTER(_p), _i, _p, _i, _i64, _i64, _p, ctypes.POINTER(_p),

@@ -25,6 +25,7 @@ __all__ = [
     "tq_quant_paged", "tq_attn_decode_paged", "tq_quant_gather_groups", "tq_attn_prefill",
     "tq_attn_prefill_workspace", "TQ_POLAR", "tq_polar_codebook", "tq_create_polar", "tq_quant_polar",
     "tq_dequant_polar", "TQ_KV8", "TQ_STATUS_RANGE", "tq_create_kv8", "tq_quant_kv8", "tq_dequant_kv8",
+    "tq_attn_prompt", "tq_attn_prompt_workspace", "tq_attn_tree", "tq_attn_tree_workspace",
 ]
 
 
@@ -419,6 +420,95 @@ def tq_dequant_kv8(h: Handle, slots: torch.Tensor, kcodes: torch.Tensor, kscales
     check("tq_dequant_kv8", lib.tq_dequant_kv8(h.ptr, n, _ptr(slots), _ptr(kcodes), _ptr(kscales), _ptr(vcodes),
                                                _ptr(vscales), rows, _ptr(k), _ptr(v), _dtype3(k),
                                                _stream_on(stream, k)))
+
+
+# ---- attention over prompts and over the 8-bit cache
+
+def _scratch(nbytes: int, like: torch.Tensor, stream):
+    """A workspace that belongs to the stream the call runs on (so that it may be
+    freed when the call returns), or None where none is needed."""
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_on(stream, like), device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
+def _outputs(q: torch.Tensor, out: torch.Tensor, lse) -> None:
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError(f"out: expected {tuple(q.shape)} {q.dtype}, got {tuple(out.shape)} {out.dtype}")
+    if lse is not None and (lse.shape != q.shape[:-1] or lse.dtype != torch.float32):
+        raise ValueError(f"lse: expected float32 {tuple(q.shape[:-1])}, got {lse.dtype} {tuple(lse.shape)}")
+
+
+def tq_attn_prompt_workspace(h: Handle, nseq: int, total: int, Hq: int, Hkv: int) -> int:
+    return int(lib.tq_attn_prompt_workspace(h.ptr, nseq, total, Hq, Hkv))
+
+
+def tq_attn_prompt(h: Handle, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                   scale: float, out: torch.Tensor, lse=None, workspace=None, stream=None) -> None:
+    """Causal attention over packed prompts: q [total][Hq][d], k and v
+    [total][Hkv][d] (bfloat16 or float16, a token stride allowed), sequence s in
+    tokens cu_seqlens[s] .. cu_seqlens[s+1]-1 (int32 [nseq+1]); out
+    [total][Hq][d], lse [total][Hq] float32.  h gives d: any handle."""
+    _same_device(q, k, v, cu_seqlens, out, lse, workspace)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k: expected [tokens][heads][d]")
+    total, Hq, Hkv = q.shape[0], q.shape[1], k.shape[1]
+    strides = _token_rows(q, "q", Hq, h.d), _token_rows(k, "k", Hkv, h.d), _token_rows(v, "v", Hkv, h.d)
+    if k.shape[0] != total or v.shape[0] != total or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v: expected the same tokens and one type")
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens: expected int32 [nseq + 1]")
+    _outputs(q, out, lse)
+    nseq = cu_seqlens.numel() - 1
+    if workspace is None:
+        workspace = _scratch(tq_attn_prompt_workspace(h, nseq, total, Hq, Hkv), q, stream)
+    check("tq_attn_prompt", lib.tq_attn_prompt(
+        h.ptr, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype3(q), _ptr(cu_seqlens), nseq, total, Hq, Hkv, *strides,
+        float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_on(stream, q)))
+
+
+def tq_attn_tree_workspace(h: Handle, B: int, n: int, Hq: int, Hkv: int) -> int:
+    return int(lib.tq_attn_tree_workspace(h.ptr, B, n, Hq, Hkv))
+
+
+def tq_attn_tree(h: Handle, q: torch.Tensor, Hkv: int, ctx_lens: torch.Tensor, block_table: torch.Tensor,
+                 page_size: int, kcodes: torch.Tensor, kscales: torch.Tensor, vcodes: torch.Tensor,
+                 vscales: torch.Tensor, scale: float, out: torch.Tensor, lse=None, mask=None, draft_lens=None,
+                 workspace=None, stream=None) -> None:
+    """Attention of n drafted tokens per sequence, q [B][n][Hq][d] (bfloat16 or
+    float16), over the 8-bit paged cache: ctx_lens [B] context tokens that all
+    of them see, then draft_lens [B] (n each if None) drafted ones, of which
+    token i sees those in its bits mask [B][n][ceil(n/32)] (int32; a chain if
+    None); block_table is [B*Hkv][max_pages] int32."""
+    _same_device(q, ctx_lens, block_table, kcodes, kscales, vcodes, vscales, out, lse, mask, draft_lens, workspace)
+    if q.dim() != 4 or q.shape[3] != h.d:
+        raise ValueError(f"q: expected [B][n][Hq][{h.d}], got {tuple(q.shape)}")
+    B, n, Hq, d = q.shape
+    # tokens a constant number of elements apart, each with its heads side by side
+    qs = q.stride(1) if n > 1 else q.stride(0) if B > 1 else Hq * d
+    if q.numel() and (q.stride(3) != 1 or (Hq > 1 and q.stride(2) != d) or (B > 1 and n > 1 and q.stride(0) != n * qs)):
+        raise ValueError("q: tokens must lie a constant stride apart, their heads side by side")
+    for name, t, shape in (("ctx_lens", ctx_lens, (B,)), ("draft_lens", draft_lens, (B,)),
+                           ("mask", mask, (B, n, (n + 31) // 32))):
+        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape):
+            raise ValueError(f"{name}: expected int32 {shape}, got {t.dtype} {tuple(t.shape)}")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B * Hkv:
+        raise ValueError(f"block_table: expected int32 [{B * Hkv}][max_pages], got {block_table.dtype} {tuple(block_table.shape)}")
+    rows = _cache_rows(h, kcodes, kscales, vcodes, vscales)
+    _outputs(q, out, lse)
+    if workspace is None:
+        workspace = _scratch(tq_attn_tree_workspace(h, B, n, Hq, Hkv), q, stream)
+    check("tq_attn_tree", lib.tq_attn_tree(
+        h.ptr, q.data_ptr(), _dtype3(q), qs, B, n, Hq, Hkv, _ptr(ctx_lens), _ptr(draft_lens), _ptr(mask),
+        _ptr(block_table), block_table.shape[1], page_size, _ptr(kcodes), _ptr(kscales), _ptr(vcodes), _ptr(vscales),
+        rows, float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_on(stream, q)))
 
 
 def tq_device_status(h: Handle) -> int:

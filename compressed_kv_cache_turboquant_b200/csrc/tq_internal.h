@@ -270,6 +270,33 @@ int launch_kv8_write(const tq_ctx* h, const void* k, const void* v, int dtype, i
 int launch_kv8_read(const tq_ctx* h, int64_t N, const int64_t* slots, const int8_t* kcodes, const float* kscales,
                     const int8_t* vcodes, const float* vscales, int64_t rows, void* k, void* v, int dtype,
                     void* stream);
+// attention of drafted tokens over the 8-bit paged cache (tq_attn_tree)
+struct TreeArgs {
+  const void* q;
+  int64_t q_stride;
+  int B, n, Hq, Hkv, d;
+  const int32_t* ctx_lens;
+  const int32_t* draft_lens;  // NULL: n each
+  const uint32_t* mask;       // NULL: a chain
+  const int32_t* block_table;
+  int max_pages, page;
+  const int8_t* kcodes;
+  const float* kscales;
+  const int8_t* vcodes;
+  const float* vscales;
+  int64_t rows;               // rows of the cache
+  float scale_log2;           // logit scale * log2(e)
+  void* out;
+  float* lse;
+  int* status;
+};
+size_t tree_workspace(const tq_ctx* h, int B, int n, int Hq, int Hkv);
+int launch_tree(const tq_ctx* h, const TreeArgs& a, int dtype, void* workspace, void* stream);
+// causal attention over packed prompts (tq_attn_prompt)
+size_t prompt_workspace(const tq_ctx* h, int nseq, int64_t total, int Hq, int Hkv);
+int launch_prompt(const tq_ctx* h, const void* q, const void* k, const void* v, int dtype, const int32_t* cu, int nseq,
+                  int64_t total, int Hq, int Hkv, int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                  void* out, float* lse, void* workspace, void* stream);
 // decode attention through whichever kernel fits; workspace layout owned here.
 // partial_out: write the (acc[d] in the rotated value frame, m, l) record of
 // every (batch, q-head) to out [B*Hq][d + 2] instead of the normalised output

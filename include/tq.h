@@ -357,6 +357,38 @@ TQ_API int tq_attn_prefill(tq_handle hk, tq_handle hv, const void* q, int q_dtyp
                            float scale, float* out, void* workspace, size_t ws_bytes, void* stream);
 TQ_API size_t tq_attn_prefill_workspace(tq_handle hk, int B, int nq, int Hq, int Hkv, int64_t T);
 
+/*
+ * tq_attn_prompt -- causal attention over whole prompts, packed one behind the
+ * other, before anything is compressed (a prompt's own attention runs on the
+ * exact keys and values; [tq.net, "实现步骤草图", 集成到 attention] compresses them
+ * for the steps after it).  Sequence s holds tokens cu_seqlens[s] ..
+ * cu_seqlens[s+1] - 1; for its token i and query head j (kv-head h = j / (Hq/Hkv)):
+ *   out[i][j] = sum_{t <= i, t in s} softmax(scale q_ij . k_th) v_th
+ *   lse[i][j] = log sum_{t <= i, t in s} e^(scale q_ij . k_th)
+ *   h           any handle: its dimension d (<= 128) and its status word are used
+ *   q, k, v     dev in, [total][Hq or Hkv][d] of `dtype` (TQ_BF16 or TQ_F16): head
+ *               h of token t at q + t*q_stride + h*d elements (strides >= heads * d
+ *               and a multiple of 8; not looked at for total <= 1), so slices of
+ *               one fused projection do
+ *   cu_seqlens  dev in, [nseq + 1] int32 ascending (a captured call replays with
+ *               other lengths); an empty sequence has no rows.  Bounds outside
+ *               0..total, or below an earlier one, count as the nearest that is not
+ *   scale       logit scale, >= 0
+ *   out         dev out, [total][Hq][d] of `dtype`;  lse  dev out, [total][Hq]
+ *               float32, or NULL.  Tokens of no sequence (before the first, behind
+ *               the last) are neither read nor written
+ *   workspace   dev scratch of at least tq_attn_prompt_workspace(...) bytes
+ * An infinity or NaN in a key or value reaches only the tokens that see it.
+ * Supported: Hq / Hkv <= 128, nseq <= TQ_MAX_SEQS, total <= 2^31 / 128.
+ * Errors: TQ_EINVAL, TQ_EUNSUPPORTED, TQ_EALIGN, TQ_EWORKSPACE, TQ_ECUDA.
+ */
+#define TQ_MAX_SEQS 4096
+TQ_API int tq_attn_prompt(tq_handle h, const void* q, const void* k, const void* v, int dtype,
+                          const int32_t* cu_seqlens, int nseq, int64_t total, int Hq, int Hkv, int64_t q_stride,
+                          int64_t k_stride, int64_t v_stride, float scale, void* out, float* lse, void* workspace,
+                          size_t ws_bytes, void* stream);
+TQ_API size_t tq_attn_prompt_workspace(tq_handle h, int nseq, int64_t total, int Hq, int Hkv);
+
 /* ---------------------------------------------------------------- a cache split across devices */
 
 /*
@@ -514,6 +546,47 @@ TQ_API int tq_quant_kv8(tq_handle h, const void* k, const void* v, int dtype, in
 TQ_API int tq_dequant_kv8(tq_handle h, int64_t n, const int64_t* slots, const int8_t* kcodes, const float* kscales,
                           const int8_t* vcodes, const float* vscales, int64_t rows, void* k, void* v, int out_dtype,
                           void* stream);
+
+/*
+ * tq_attn_tree -- attention of the drafted tokens of every sequence over the
+ * 8-bit paged cache that already holds them: sequence b has ctx_lens[b] context
+ * tokens at places 0 .. ctx-1 of its pages and draft_lens[b] drafted ones behind
+ * them.  Every drafted token sees the whole context; token i sees drafted token
+ * j iff bit j of its mask is set (itself among them, if its bit is).  n = 1 is
+ * the decode step.  For token i, query head j (kv-head h = j / (Hq/Hkv)):
+ *   out[b][i][j] = sum_t softmax(scale q_bij . k_t) v_t over the seen t, and
+ *   lse[b][i][j] = log sum_t e^(scale q_bij . k_t), k_t = c s of its cache row
+ *   h            a TQ_KV8 handle
+ *   q            dev in, [B][n][Hq][d] of `dtype` (TQ_BF16 or TQ_F16), head j of
+ *                token i at q + (b*n + i)*q_stride + j*d elements (a multiple of 8,
+ *                >= Hq d; not looked at for B n <= 1)
+ *   ctx_lens     dev in, [B] int32;  draft_lens  dev in, [B] int32, or NULL: n each.
+ *                Rows of tokens past draft_lens[b] are not written
+ *   mask         dev in, [B][n][ceil(n/32)] words, bit j of token i at word j / 32,
+ *                or NULL: a chain (token i sees j <= i)
+ *   block_table  dev in, [B*Hkv][max_pages] int32 as in tq_attn_decode_paged;
+ *                page_size a multiple of 8
+ *   kcodes, kscales, vcodes, vscales   dev in, the cache (`rows` rows)
+ *   scale        logit scale, >= 0
+ *   out          dev out, [B][n][Hq][d] of `dtype`;  lse  dev out, [B][n][Hq]
+ *                float32, or NULL
+ *   workspace    dev scratch of at least tq_attn_tree_workspace(...) bytes (0 for
+ *                none); calls that may overlap need one each
+ * A token that sees nothing gives out = 0 and lse = -infinity.  Lengths that
+ * are negative or pass the block table, and page ids outside the cache, count
+ * as absent keys and set TQ_STATUS_RANGE.  Codes and scales of keys that a token
+ * does not see have no part in its result, whatever they hold.
+ * Supported: n <= TQ_MAX_DRAFT, B <= TQ_MAX_SEQS, rows < 2^31 - 4096
+ * (TQ_EUNSUPPORTED otherwise).
+ * Errors: TQ_EINVAL, TQ_EUNSUPPORTED, TQ_EALIGN, TQ_EWORKSPACE, TQ_ECUDA.
+ */
+#define TQ_MAX_DRAFT 256
+TQ_API int tq_attn_tree(tq_handle h, const void* q, int dtype, int64_t q_stride, int B, int n, int Hq, int Hkv,
+                        const int32_t* ctx_lens, const int32_t* draft_lens, const uint32_t* mask,
+                        const int32_t* block_table, int max_pages, int page_size, const int8_t* kcodes,
+                        const float* kscales, const int8_t* vcodes, const float* vscales, int64_t rows, float scale,
+                        void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+TQ_API size_t tq_attn_tree_workspace(tq_handle h, int B, int n, int Hq, int Hkv);
 
 /* ---------------------------------------------------------------- channel groups */
 
