@@ -25,6 +25,11 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xc
               "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
 
+# Kernels that move registers between their warpgroups (setmaxnreg): the
+# assembler only does that in a unit compiled as a whole program.
+WHOLE_PROGRAM = {"attn_tree.cu", "attn_prompt.cu"}
+
+
 def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
 
@@ -45,7 +50,8 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
         deps = [src] + [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".h", ".cuh"))]
         deps.append(os.path.join(ROOT, "include", "tq.h"))
         if force or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(p) for p in deps):
-            cmd = [nvcc(), *ARCH, *NVCC_FLAGS, "-dc" if src.endswith(".cu") else "-c",
+            separate = src.endswith(".cu") and os.path.basename(src) not in WHOLE_PROGRAM
+            cmd = [nvcc(), *ARCH, *NVCC_FLAGS, "-dc" if separate else "-c",
                    "-x", "cu" if src.endswith(".cu") else "c++", src, "-o", obj]
             if ptxas_verbose and src.endswith(".cu"):
                 cmd[1:1] = ["-Xptxas", "-v"]
