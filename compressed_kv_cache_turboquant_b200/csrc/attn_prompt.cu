@@ -1,12 +1,42 @@
-// Causal attention over a whole prompt batch (packed sequences) before anything
-// is compressed.  One warp per (token, query head): lanes hold the query and
-// the running value sum, keys go by one at a time, with the running maximum and
-// sum of the softmax in float32.
+// Causal attention over packed prompts on the tensor cores (sm_100a).
+//
+// turboquant.net/zh, "实现步骤草图", 集成到 attention: the cache is compressed for the
+// steps after the prompt; the prompt's own attention runs on the exact keys and
+// values.  With a softmax in base 2 (c = scale log2 e, m_i a running reference
+// of row i's largest logit),
+//   S = Q K^T,  P = 2^(c S - m),  O += P V,  l += sum P,
+//   out = O / l,  lse = (m + log2 l) ln 2.
+// A row is a (token, head of a kv-head's group) pair: 128 / G tokens of a group
+// of G heads fill the 128 rows of a tile, so every key tile serves all heads of
+// its group.  A work item is two such row tiles of one sequence and kv-head, and
+// the key tiles of 128 up to its last token.
+//
+// Q and K tiles are shared-memory operands, S and O accumulate in tensor memory,
+// and P overwrites the first half of its S as the tensor-memory operand of the
+// value product.  The two row tiles take turns: while one's softmax runs on the
+// CUDA cores, the tensor cores work for the other.  P is the inputs' type (one
+// rounding of 2^-9 or 2^-12 relative; l sums the unrounded weights).
+//
+// Warps (384 threads, one block per SM, persistent over the items):
+//   0-3, 4-7  softmax of row tile 0, 1: thread = row (TMEM lane); the reference
+//             moves, and O is rescaled, only when a logit passes it by 2^8
+//   8         TMA: the item's Q tiles, then K and V tiles through a ring
+//   9         the single-thread MMA issuer
+//   10, 11    look through the V tiles that some row does not see whole: an
+//             infinity or NaN there, times a weight of 0, would spoil rows that
+//             must not see it.  Such elements become 0 in shared memory, and the
+//             rows that do see them add them at the end (a bit per key)
+//
+// Items are sorted by length of their key range, longest first, by a one-block
+// kernel (prompt_plan_kernel); a grid with no more items than blocks finds them
+// itself.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "sm100_common.cuh"
 #include "tq_internal.h"
@@ -14,92 +44,665 @@
 namespace tqi {
 namespace {
 
-struct PromptArgs {
-  const void* q;
-  const void* k;
-  const void* v;
-  const int32_t* cu;
-  void* out;
-  float* lse;
-  int64_t total, q_stride, k_stride, v_stride;
-  int nseq, Hq, Hkv, d;
-  float scale_log2;
+using namespace sm100;
+
+constexpr int kTile = 128;                 // rows of a row tile, keys of a key tile
+constexpr int kThreads = 384;
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;   // 2 x 208 + 88 = 3 x 168, the registers at launch
+constexpr uint32_t kColS = 0, kColO = 256; // S/P of tiles 0, 1 at 0, 128; O at 256, 384
+constexpr float kLazy = 8.f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr int kBadSlots = 8;               // items whose bad-key bits are kept (more than the ring can run ahead)
+constexpr int kBadTiles = 4;               // key tiles of an item that some row does not see whole: 3 at most
+constexpr int kBuckets = 1024;
+
+template <int D>
+struct Shape {
+  static constexpr int slabs = D / 64;
+  static constexpr int tile = kTile * D * 2;           // bytes of a Q, K or V tile
+  static constexpr int stages = D == 128 ? 4 : 8;
+  static constexpr int off_ring = 2 * tile;
+  static constexpr int off_bad = off_ring + stages * tile;   // [kBadSlots][1 + 4 kBadTiles] words
+  static constexpr int off_bar = off_bad + kBadSlots * (1 + 4 * kBadTiles) * 4;
+  static constexpr int bytes = (off_bar + 320 + 16 + 1023) / 1024 * 1024 + 1024;
 };
 
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_float(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_float(__half* p, float x) { *p = __float2half_rn(x); }
+struct PromptArgs {
+  const void* v;
+  void* out;
+  float* lse;
+  const int32_t* cu;
+  const int4* items;      // (first token, tokens, item of the sequence, 0), by key range
+  const int32_t* count;   // items
+  int64_t v_stride;
+  int total, nseq, Hq, Hkv, d, G, tq;   // tq = 128 / G tokens of a row tile
+  int direct;             // no plan: block i finds item i / Hkv
+  float scale_log2;
+  int* status;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// an MN-major operand in the 128-byte swizzled layout: 128-byte rows of 64
+// elements along N, 8-row atoms 1024 bytes apart along K, the next 64 elements
+// of N lbo bytes further
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+// keeps every use of registers that tcgen05.ld fills behind its wait
+__device__ __forceinline__ void regs_after_wait(float (&r)[32]) {
+  asm volatile(""
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])::"memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack(float lo, float hi, __nv_bfloat16) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi, __half) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 template <typename T>
-__global__ void __launch_bounds__(128) prompt_rows_kernel(PromptArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int64_t t = w / a.Hq;
-  const int hq = (int)(w % a.Hq), hk = hq / (a.Hq / a.Hkv);
-  if (t >= a.total) return;
-  // the sequence of token t: bounds never decrease here, whatever the array holds
-  int64_t lo = -1, prev = min((int64_t)max(a.cu[0], 0), a.total);
-  for (int s = 0; s < a.nseq; ++s) {
-    const int64_t end = max(prev, min((int64_t)a.cu[s + 1], a.total));
-    if (t >= prev && t < end) {
-      lo = prev;
-      break;
+struct Bits;   // exponent bits of a 16-bit element, and what lifts them into the sign when all are set
+template <>
+struct Bits<__nv_bfloat16> {
+  static constexpr uint32_t exponent = 0x7F807F80u, one = 0x00800080u;
+};
+template <>
+struct Bits<__half> {
+  static constexpr uint32_t exponent = 0x7C007C00u, one = 0x04000400u;
+};
+
+// sign bits of the halves that are infinite or NaN
+template <typename T>
+__device__ __forceinline__ uint32_t bad_halves(uint32_t w) {
+  return ((w & Bits<T>::exponent) + Bits<T>::one) & 0x80008000u;
+}
+
+struct Item {
+  int start, len;   // the sequence's first token and tokens
+  int h;
+  int tok[2];       // first token of each row tile, in the sequence
+  int n[2];         // key tiles of each (0: no rows)
+  int tiles;        // key tiles to load
+};
+
+// Lists the items of all sequences (one every 2 tq tokens), the longest key
+// ranges first.  Bounds that fall below an earlier one or leave 0..total count
+// as the nearest that do not, so the sequences never overlap and the list never
+// holds more than total / (2 tq) + nseq items.
+__global__ void __launch_bounds__(1024) prompt_plan_kernel(const int32_t* cu, int nseq, int total, int per_item,
+                                                           int4* items, int32_t* count) {
+  __shared__ int bound[4097];
+  __shared__ int before[4097];              // items of the sequences before
+  __shared__ int bucket[kBuckets];
+  __shared__ int warp_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // running maximum of the clamped bounds, then running sums of the items: 1024 at a time
+  int carry = 0;
+  for (int b0 = 0; b0 <= nseq; b0 += 1024) {
+    const int i = b0 + tid;
+    int v = i <= nseq ? min(max(cu[i], 0), total) : 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, v, o);
+      if (lane >= o) v = max(v, x);
     }
-    prev = end;
+    if (lane == 31) warp_sum[warp] = v;
+    __syncthreads();
+    int m = carry;
+    for (int w = 0; w < warp; ++w) m = max(m, warp_sum[w]);
+    v = max(v, m);
+    if (i <= nseq) bound[i] = v;
+    for (int w = 0; w < 32; ++w) carry = max(carry, warp_sum[w]);
+    __syncthreads();
   }
-  if (lo < 0) return;
-  const T* q = static_cast<const T*>(a.q) + t * a.q_stride + (int64_t)hq * a.d;
-  float qv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) qv[i] = lane + 32 * i < a.d ? to_float(q[lane + 32 * i]) : 0.f;
-  float m = -INFINITY, l = 0.f;
-  for (int64_t j = lo; j <= t; ++j) {
-    const T* k = static_cast<const T*>(a.k) + j * a.k_stride + (int64_t)hk * a.d;
-    const T* v = static_cast<const T*>(a.v) + j * a.v_stride + (int64_t)hk * a.d;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 32 * i < a.d) s = fmaf(qv[i], to_float(k[lane + 32 * i]), s);
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    s *= a.scale_log2;
-    if (s > m || s != s) {
-      const float alpha = exp2f(m - s);
-      l *= alpha;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] *= alpha;
-      m = s;
+  carry = 0;
+  for (int b0 = 0; b0 < nseq; b0 += 1024) {
+    const int i = b0 + tid;
+    const int own = i < nseq ? (bound[i + 1] - bound[i] + per_item - 1) / per_item : 0;
+    int v = own;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, v, o);
+      if (lane >= o) v += x;
     }
-    const float p = m == -INFINITY ? 0.f : exp2f(s - m);
-    l += p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 32 * i < a.d) acc[i] = fmaf(p, to_float(v[lane + 32 * i]), acc[i]);
+    if (lane == 31) warp_sum[warp] = v;
+    __syncthreads();
+    int m = carry;
+    for (int w = 0; w < warp; ++w) m += warp_sum[w];
+    if (i < nseq) before[i] = m + v - own;
+    for (int w = 0; w < 32; ++w) carry += warp_sum[w];
+    __syncthreads();
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* out = static_cast<T*>(a.out) + (t * a.Hq + hq) * a.d;
+  const int n = carry;
+  if (tid == 0) before[nseq] = n, *count = n;
+  bucket[tid] = 0;
+  __syncthreads();
+  // a bucket per key-range length (or so many of them alike that 1024 do)
+  const int span = (total + per_item - 1) / per_item / kBuckets + 1;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int i = tid; i < n; i += 1024) {
+      int lo = 0, hi = nseq;                 // the last sequence with before <= i that has items
+      while (lo + 1 < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (before[mid] <= i) lo = mid; else hi = mid;
+      }
+      const int at = i - before[lo];
+      int* b = &bucket[min(at / span, kBuckets - 1)];
+      const int place = atomicAdd(b, 1);
+      if (pass) items[place] = make_int4(bound[lo], bound[lo + 1] - bound[lo], at, 0);
+    }
+    __syncthreads();
+    if (pass == 0) {
+      // the longest first: a bucket begins behind all longer ones
+      const int r = kBuckets - 1 - tid, own = bucket[r];
+      int v = own;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += x;
+      }
+      if (lane == 31) warp_sum[warp] = v;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) v += warp_sum[w];
+      bucket[r] = v - own;
+      __syncthreads();
+    }
+  }
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+              const __grid_constant__ CUtensorMap vmap, PromptArgs a) {
+  using S = Shape<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = smem + S::off_ring;
+  uint32_t* bad = reinterpret_cast<uint32_t*>(smem + S::off_bad);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::off_bar);   // [stages] tx
+  uint64_t* empty = full + S::stages;    // [stages] MMA commit and both scanning warps
+  uint64_t* q_full = empty + S::stages;  // tx
+  uint64_t* q_free = q_full + 1;         // MMA commit: the item's logit products are done
+  uint64_t* clean = q_free + 1;          // [stages] both scanning warps: looked through, where it needs that
+  uint64_t* s_full = clean + S::stages;       // [2] MMA commit: logits of a tile
+  uint64_t* p_ready = s_full + 2;        // [2] 4 softmax warps: weights written
+  uint64_t* pv_done = p_ready + 2;       // [2] MMA commit: value product done
+  uint64_t* done = pv_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  int4* direct_item = reinterpret_cast<int4*>(smem + S::off_bar + 320);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 3);
+      mbar_init(&clean[s], 2);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_free, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_ready[t], 4);
+      mbar_init(&pv_done[t], 1);
+    }
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  if (a.direct && warp == 0) {
+    // the sequence of item blockIdx.x / Hkv, with the plan's reading of the bounds
+    int left = blockIdx.x / a.Hkv, prev = min(max(__ldg(a.cu), 0), a.total);
+    int4 found = make_int4(0, 0, -1, 0);
+    const int per_item = 2 * a.tq;
+    for (int s0 = 0; s0 < a.nseq && found.z < 0; s0 += 32) {
+      int v = s0 + lane < a.nseq ? min(max(__ldg(a.cu + s0 + lane + 1), 0), a.total) : 0;
+      v = max(v, prev);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v = max(v, x);
+      }
+      int first = __shfl_up_sync(kFull, v, 1);
+      if (lane == 0) first = prev;
+      const int own = (v - first + per_item - 1) / per_item;
+      int upto = own;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const uint32_t past = __ballot_sync(kFull, upto > left);
+      if (past) {
+        const int who = __ffs(past) - 1;
+        found = make_int4(__shfl_sync(kFull, first, who), __shfl_sync(kFull, v - first, who),
+                          left - __shfl_sync(kFull, upto - own, who), 0);
+      } else {
+        left -= __shfl_sync(kFull, upto, 31);
+        prev = __shfl_sync(kFull, v, 31);
+      }
+    }
+    if (lane == 0) *direct_item = found;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // the block's i-th item; every role walks the same ones
+  const int all = a.direct ? 0 : *a.count * a.Hkv;
+  auto item = [&](int i, Item& it) -> bool {
+    int4 e;
+    if (a.direct) {
+      if (i > 0) return false;
+      e = *direct_item;
+      if (e.z < 0) return false;
+      it.h = blockIdx.x % a.Hkv;
+    } else {
+      // there and back over the sorted list, so that the blocks' sums stay close
+      const int x = i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (x >= all) return false;
+      e = __ldg(a.items + x / a.Hkv);
+      it.h = x % a.Hkv;
+    }
+    it.start = e.x;
+    it.len = e.y;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < a.d) from_float(out + lane + 32 * i, acc[i] * inv);
-  if (a.lse && lane == 0) a.lse[t * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    for (int t = 0; t < 2; ++t) {
+      it.tok[t] = (e.z * 2 + t) * a.tq;
+      it.n[t] = it.tok[t] < it.len ? (min(it.tok[t] + a.tq, it.len) - 1) / kTile + 1 : 0;
+    }
+    it.tiles = max(it.n[0], it.n[1]);
+    return true;
+  };
+  // the first key tile that some row of the item does not see whole
+  auto first_cut = [&](const Item& it) { return (it.tok[0] + 1) / kTile; };
+  Item it;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 8) {
+      // ---------------- TMA
+      if (lane == 0) {
+        int st = 0;
+        bool ok = true;
+        for (int i = 0; ok && item(i, it); ++i) {
+          auto load = [&](const CUtensorMap* map, int j) -> bool {
+            const int s = st % S::stages;
+            if (!mbar_wait(&empty[s], (uint32_t)(((st / S::stages) & 1) ^ 1))) return false;
+            mbar_arrive_expect_tx(&full[s], S::tile);
+            for (int sl = 0; sl < S::slabs; ++sl)
+              tma_load_3d(map, &full[s], ring + s * S::tile + sl * kTile * 128, sl * 64, it.h, it.start + j * kTile);
+            ++st;
+            return true;
+          };
+          if (i > 0 && !mbar_wait(q_free, (uint32_t)((i - 1) & 1))) ok = false;
+          if (ok) {
+            const int rows = a.G * a.tq;
+            mbar_arrive_expect_tx(q_full, (uint32_t)((it.n[1] ? 2 : 1) * S::slabs * rows * 128));
+            for (int t = 0; t < (it.n[1] ? 2 : 1); ++t)
+              for (int sl = 0; sl < S::slabs; ++sl)
+                tma_load_3d(&qmap, q_full, smem + t * S::tile + sl * kTile * 128, sl * 64, it.h * a.G,
+                            it.start + it.tok[t]);
+          }
+          for (int j = 0; ok && j < it.tiles; ++j) ok = load(&kmap, j) && load(&vmap, j);
+        }
+        if (!ok) atomicOr(a.status, kStatusTimeout);
+        // no copy may still be in flight when the block ends
+        for (int x = st > S::stages ? st - S::stages : 0; x < st; ++x)
+          if (!mbar_wait(&full[x % S::stages], (uint32_t)((x / S::stages) & 1))) atomicOr(a.status, kStatusTimeout);
+      }
+    } else if (warp == 9) {
+      // ---------------- MMA
+      if (lane == 0) {
+        constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+        const uint32_t idesc_s = idesc_f16(kTile, kTile, bf), idesc_o = idesc_f16(kTile, D, bf) | (1u << 16);
+        const uint32_t qb = smem_u32(smem), rb = smem_u32(ring);
+        int st = 0, pv[2] = {0, 0};
+        bool ok = true;
+        auto wait_full = [&](int x) { return mbar_wait(&full[x % S::stages], (uint32_t)((x / S::stages) & 1)); };
+        // S of tile t from the K tile of ring step x; the buffer's last P must have been consumed
+        auto logits = [&](int t, int x) -> bool {
+          if (pv[t] > 0 && !mbar_wait(&pv_done[t], (uint32_t)((pv[t] - 1) & 1))) return false;
+          tc_fence_after();
+          const uint32_t kb = rb + (x % S::stages) * S::tile, q = qb + t * S::tile;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (uint32_t)((ks >> 2) * kTile * 128 + (ks & 3) * 32);
+            mma_f16(tmem + kColS + t * 128, sw128_kmajor_desc(q + off), sw128_kmajor_desc(kb + off), idesc_s, ks ? 1u : 0u);
+          }
+          mma_commit(&s_full[t]);
+          return true;
+        };
+        auto values = [&](int t, int x, bool first) -> bool {
+          if (!mbar_wait(&p_ready[t], (uint32_t)(pv[t] & 1))) return false;
+          tc_fence_after();
+          const uint32_t vb = rb + (x % S::stages) * S::tile;
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            mma_f16_ta(tmem + kColO + t * 128, tmem + kColS + t * 128 + 8 * ks, sw128_mnmajor_desc(vb + ks * 2048, kTile * 128),
+                       idesc_o, (first && ks == 0) ? 0u : 1u);
+          mma_commit(&pv_done[t]);
+          ++pv[t];
+          return true;
+        };
+        for (int i = 0; ok && item(i, it); ++i) {
+          ok = mbar_wait(q_full, (uint32_t)(i & 1)) && wait_full(st) && (!it.n[0] || logits(0, st)) && (!it.n[1] || logits(1, st));
+          if (!ok) break;
+          mma_commit(&empty[st % S::stages]);
+          if (it.tiles == 1) mma_commit(q_free);
+          const int cut = first_cut(it);
+          for (int j = 0; j < it.tiles; ++j) {
+            const int xv = st + 2 * j + 1, xk = xv + 1;
+            // a tile that some row does not see whole has to be looked through first
+            ok = wait_full(xv) && (j < cut || mbar_wait(&clean[xv % S::stages], (uint32_t)((xv / S::stages) & 1)));
+            if (!ok) break;
+            const bool more = j + 1 < it.tiles;
+            if (j < it.n[0] && !(ok = values(0, xv, j == 0))) break;
+            if (more && !(ok = wait_full(xk))) break;
+            if (j + 1 < it.n[0] && !(ok = logits(0, xk))) break;
+            if (j < it.n[1] && !(ok = values(1, xv, j == 0))) break;
+            mma_commit(&empty[xv % S::stages]);
+            if (j + 1 < it.n[1] && !(ok = logits(1, xk))) break;
+            if (more) mma_commit(&empty[xk % S::stages]);
+            if (j + 2 == it.tiles) mma_commit(q_free);
+          }
+          st += 2 * it.tiles;
+        }
+        if (!ok) atomicOr(a.status, kStatusTimeout);
+        // nothing may still run when tensor memory is given back
+        mma_commit(done);
+        if (!mbar_wait(done, 0)) atomicOr(a.status, kStatusTimeout);
+      }
+    } else {
+      // ---------------- V tiles that some row does not see whole
+      const int w = warp - 10;
+      int st = 0;
+      bool ok = true;
+      for (int i = 0; ok && item(i, it); ++i) {
+        uint32_t* bits = bad + (i % kBadSlots) * (1 + 4 * kBadTiles);
+        const int cut = first_cut(it);
+        for (int j = 0; j < it.tiles; ++j) {
+          for (int kv = 0; kv < 2; ++kv, ++st) {
+            const int s = st % S::stages;
+            if (!(ok = mbar_wait_warp(&full[s], (uint32_t)((st / S::stages) & 1)))) break;
+            if (kv && j >= cut) {
+              // lane = key of a 32-key group: two groups a warp
+              uint8_t* vt = ring + s * S::tile;
+              for (int gr = 0; gr < 2; ++gr) {
+                const int key = w * 64 + gr * 32 + lane;
+                bool any = false;
+#pragma unroll 4
+                for (int u = 0; u < D / 8; ++u) {
+                  uint4* p = reinterpret_cast<uint4*>(vt + (u >> 3) * kTile * 128 + key * 128 + (((u & 7) ^ (key & 7)) << 4));
+                  uint4 x = *p;
+                  const uint32_t b0 = bad_halves<T>(x.x), b1 = bad_halves<T>(x.y), b2 = bad_halves<T>(x.z), b3 = bad_halves<T>(x.w);
+                  if (b0 | b1 | b2 | b3) {
+                    any = true;
+                    // a set sign bit -> a half of zeros
+                    x.x &= ~((b0 >> 15) * 0xFFFFu), x.y &= ~((b1 >> 15) * 0xFFFFu);
+                    x.z &= ~((b2 >> 15) * 0xFFFFu), x.w &= ~((b3 >> 15) * 0xFFFFu);
+                    *p = x;
+                  }
+                }
+                const uint32_t m = __ballot_sync(kFull, any);
+                if (lane == 0) bits[1 + (j - cut) * 4 + w * 2 + gr] = m;
+              }
+              fence_async_smem();
+              __syncwarp();
+            }
+            // every step of the ring, so that neither side ever runs two uses of a stage ahead
+            if (lane == 0) {
+              mbar_arrive(&clean[s]);
+              mbar_arrive(&empty[s]);
+            }
+          }
+          if (!ok) break;
+        }
+      }
+      if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
+    }
+  } else {
+    // ---------------- softmax: thread = row of tile t
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int t = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t sc = tmem + lanes + kColS + t * 128, oc = tmem + lanes + kColO + t * 128;
+    const int row_tok = r / a.G, row_head = r % a.G;
+    const float cl = a.scale_log2;
+    int steps = 0;
+    bool ok = true;
+    for (int i = 0; ok && item(i, it); ++i) {
+      const int n = it.n[t];
+      if (n == 0) continue;
+      const int pos = it.tok[t] + row_tok;                  // the row's token in its sequence
+      const bool live = row_tok < a.tq && pos < it.len;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++steps) {
+        if (!(ok = mbar_wait_warp(&s_full[t], (uint32_t)(steps & 1)))) break;
+        tc_fence_after();
+        float x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(sc + 32 * c, x[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) regs_after_wait(x[c]);
+        const int lim = pos - j * kTile;                    // keys past it take no part
+        if (__any_sync(kFull, lim < kTile - 1)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[c][e] = 32 * c + e <= lim ? x[c][e] : -INFINITY;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = max3(x[c][0], x[c][1], x[c][2]);
+#pragma unroll
+          for (int e = 3; e + 1 < 32; e += 2) mx[c] = max3(mx[c], x[c][e], x[c][e + 1]);
+          mx[c] = fmaxf(mx[c], x[c][31]);
+        }
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * cl;
+        const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
+        if (__any_sync(kFull, grow)) {
+          float f = 1.f;
+          if (grow) {
+            f = m == -INFINITY ? 0.f : ex2(m - top);
+            l *= f;
+            m = top;
+          }
+          if (j > 0) {
+            // the value product of tile j - 1 was done before this tile's logits began
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld32(oc + 32 * c, o);
+              tmem_wait_ld();
+              regs_after_wait(o);
+              uint32_t u[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(f == 0.f ? 0.f : o[e] * f);
+              tmem_st32(oc + 32 * c, u);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t u[32];
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float p0 = ex2(fmaf(x[2 * hf + c][e], cl, -ref)), p1 = ex2(fmaf(x[2 * hf + c][e + 1], cl, -ref));
+              sum[(e >> 1) & 3] += p0 + p1;
+              u[16 * c + e / 2] = pack(p0, p1, T());
+            }
+          tmem_st32(sc + 32 * hf, u);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[t]);
+      }
+      if (!ok) break;
+      if (!(ok = mbar_wait_warp(&pv_done[t], (uint32_t)((steps - 1) & 1)))) break;
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t row = (int64_t)(it.start + pos) * a.Hq + it.h * a.G + row_head;
+      T* out = static_cast<T*>(a.out) + row * a.d;
+      const uint32_t* bits = bad + (i % kBadSlots) * (1 + 4 * kBadTiles) + 1;
+      const int cut = first_cut(it);
+      uint32_t some = 0;
+      for (int x = 0; x < (it.tiles - cut) * 4; ++x) some |= bits[x];
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        tmem_ld32(oc + 32 * c, o);
+        tmem_wait_ld();
+        regs_after_wait(o);
+        if (some) {
+          // infinities and NaN that the row does see, taken out of the V tiles above
+          for (int x = 0; x < (it.tiles - cut) * 4; ++x)
+            for (uint32_t b = bits[x]; b; b &= b - 1) {
+              const int key = cut * kTile + x * 32 + __ffs(b) - 1;
+              if (!live || key > pos) continue;
+              const T* v = static_cast<const T*>(a.v) + (int64_t)(it.start + key) * a.v_stride + (int64_t)it.h * a.d;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float y = 32 * c + e < a.d ? (float)v[32 * c + e] : 0.f;
+                if (!(fabsf(y) < INFINITY)) o[e] += y;
+              }
+            }
+        }
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            if (32 * c + e < a.d) {
+              uint4 w;
+              w.x = pack(o[e] * inv, o[e + 1] * inv, T());
+              w.y = pack(o[e + 2] * inv, o[e + 3] * inv, T());
+              w.z = pack(o[e + 4] * inv, o[e + 5] * inv, T());
+              w.w = pack(o[e + 6] * inv, o[e + 7] * inv, T());
+              *reinterpret_cast<uint4*>(out + 32 * c + e) = w;
+            }
+        }
+      }
+      if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      tc_fence_before();
+    }
+    if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// [tokens][heads][d] with a token stride, as boxes of 64 coordinates x `heads`
+// heads x `tokens` tokens in 128-byte swizzled rows
+bool token_map(CUtensorMap* m, const void* base, bool bf, int d, int H, int64_t total, int64_t stride, int heads, int tokens) {
+  const EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)total};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims,
+             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// more items than this never come out of `total` tokens in `nseq` sequences
+int64_t most_items(int nseq, int64_t total, int tq) { return total / (2 * tq) + nseq; }
+
+template <int D, typename T>
+int launch_main(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const PromptArgs& a, int grid,
+                cudaStream_t st) {
+  const int e = ensure_dyn_smem(reinterpret_cast<const void*>(prompt_kernel<D, T>), Shape<D>::bytes);
+  if (e) return e;
+  prompt_kernel<D, T><<<grid, kThreads, Shape<D>::bytes, st>>>(qm, km, vm, a);
+  return (int)cudaGetLastError();
 }
 
 }  // namespace
 
-size_t prompt_workspace(const tq_ctx*, int, int64_t, int, int) { return 0; }
+size_t prompt_workspace(const tq_ctx* h, int nseq, int64_t total, int Hq, int Hkv) {
+  if (nseq == 0 || total == 0 || Hq < Hkv || Hq / Hkv > kTile) return 0;
+  const int64_t items = most_items(nseq, total, kTile / (Hq / Hkv));
+  return items * Hkv <= h->sm_count ? 0 : 256 + (size_t)items * sizeof(int4);
+}
 
 int launch_prompt(const tq_ctx* h, const void* q, const void* k, const void* v, int dtype, const int32_t* cu, int nseq,
                   int64_t total, int Hq, int Hkv, int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
                   void* out, float* lse, void* workspace, void* stream) {
-  (void)workspace;
-  PromptArgs a{q, k, v, cu, out, lse, total, q_stride, k_stride, v_stride, nseq, Hq, Hkv, h->d, scale * 1.4426950408889634f};
-  const unsigned grid = (unsigned)((total * Hq + 3) / 4);
+  PromptArgs a{};
+  const bool bf = dtype == TQ_BF16;
+  a.v = v, a.out = out, a.lse = lse, a.cu = cu;
+  a.G = Hq / Hkv, a.tq = kTile / a.G;
+  // one token has no stride of its own
+  const int64_t vs = total > 1 ? v_stride : (int64_t)Hkv * h->d;
+  a.v_stride = vs, a.total = (int)total, a.nseq = nseq, a.Hq = Hq, a.Hkv = Hkv, a.d = h->d;
+  // never 0: masked logits are -infinity before they are scaled, and 0 times that is NaN
+  a.scale_log2 = std::max(scale * 1.4426950408889634f, 1e-37f);
+  a.status = h->dev.status;
+  CUtensorMap qm, km, vm;
+  if (!token_map(&qm, q, bf, h->d, Hq, total, total > 1 ? q_stride : (int64_t)Hq * h->d, a.G, a.tq) ||
+      !token_map(&km, k, bf, h->d, Hkv, total, total > 1 ? k_stride : (int64_t)Hkv * h->d, 1, kTile) ||
+      !token_map(&vm, v, bf, h->d, Hkv, total, vs, 1, kTile))
+    return (int)cudaErrorInvalidValue;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == TQ_BF16)
-    prompt_rows_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(a);
-  else
-    prompt_rows_kernel<__half><<<grid, 128, 0, st>>>(a);
-  return (int)cudaGetLastError();
+  const int64_t work = most_items(nseq, total, a.tq) * Hkv;
+  a.direct = work <= h->sm_count;
+  if (!a.direct) {
+    a.count = static_cast<const int32_t*>(workspace);
+    a.items = reinterpret_cast<const int4*>(static_cast<char*>(workspace) + 256);
+    prompt_plan_kernel<<<1, 1024, 0, st>>>(cu, nseq, (int)total, 2 * a.tq, const_cast<int4*>(a.items),
+                                           const_cast<int32_t*>(a.count));
+    const int e = (int)cudaGetLastError();
+    if (e) return e;
+  }
+  const int grid = (int)std::min<int64_t>(work, h->sm_count);
+  if (h->d <= 64)
+    return bf ? launch_main<64, __nv_bfloat16>(qm, km, vm, a, grid, st) : launch_main<64, __half>(qm, km, vm, a, grid, st);
+  return bf ? launch_main<128, __nv_bfloat16>(qm, km, vm, a, grid, st) : launch_main<128, __half>(qm, km, vm, a, grid, st);
 }
 
 }  // namespace tqi
@@ -124,7 +727,7 @@ extern "C" int tq_attn_prompt(tq_handle h, const void* q, const void* k, const v
     return set_error(TQ_EINVAL, "%s: bad shape (nseq=%d total=%lld Hq=%d Hkv=%d)", fn, nseq, (long long)total, Hq, Hkv);
   if (Hq / Hkv > 128) return set_error(TQ_EUNSUPPORTED, "%s: %d query heads per kv-head (at most 128)", fn, Hq / Hkv);
   if (nseq > TQ_MAX_SEQS) return set_error(TQ_EUNSUPPORTED, "%s: nseq = %d (at most %d)", fn, nseq, TQ_MAX_SEQS);
-  if (total > INT32_MAX / 128 || total * Hkv > INT32_MAX / 2)
+  if (total > INT32_MAX / 128 || (total + nseq) * Hkv > INT32_MAX / 2)
     return set_error(TQ_EUNSUPPORTED, "%s: total = %lld tokens of %d kv-heads", fn, (long long)total, Hkv);
   if (!std::isfinite(scale) || scale < 0.f) return set_error(TQ_EINVAL, "%s: scale is negative or not finite", fn);
   if (nseq == 0 || total == 0 || Hq == 0) return clear_error();
