@@ -14,10 +14,11 @@
 // gets s = NaN and codes 0, so that what reads it gets NaN in that row alone.
 //
 // Both directions are bound by HBM: d e + d + 4 bytes a row and tensor, plus 8
-// of the slot list (e: bytes of an element of x).  Eight elements a thread make
-// every load of 16-bit inputs, and every store of 16-bit outputs, a whole
-// 16-byte unit of neighbouring lanes; four rows a thread keep their loads in
-// flight together.
+// of the slot list (e: bytes of an element of x).  A thread takes two pieces of
+// eight elements, `lanes` pieces apart, so that neighbouring lanes read and
+// write neighbouring 16 (or 8) bytes, of each of four rows, whose loads are in
+// flight together; what a row needs once (its maximum, its scale, 1 / s) is
+// spread over sixteen elements.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -49,14 +50,36 @@ struct Kv8Args {
   int* status;
 };
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// eight elements as they lie in memory
+template <typename T>
+struct Raw {
+  uint4 w[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+  return r;
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+template <typename T>
+__device__ __forceinline__ Raw<T> zero_raw() {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = make_uint4(0u, 0u, 0u, 0u);
+  return r;
+}
+
+__device__ __forceinline__ void floats_of(const Raw<float>& r, float (&v)[8]) {
+  const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+}
+
+__device__ __forceinline__ void floats_of(const Raw<__nv_bfloat16>& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(w[i] << 16);
@@ -64,9 +87,8 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
   }
 }
 
-__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void floats_of(const Raw<__half>& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
@@ -75,9 +97,37 @@ __device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
   }
 }
 
+// the largest |x| seen, ordered by its bits (an infinity or a NaN comes out on
+// top): of 32-bit elements in the whole word, of 16-bit ones in both halves
+__device__ __forceinline__ uint32_t raw_max(const Raw<float>& r, uint32_t m) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    m = max(m, max(r.w[i].x & 0x7FFFFFFFu, r.w[i].y & 0x7FFFFFFFu));
+    m = max(m, max(r.w[i].z & 0x7FFFFFFFu, r.w[i].w & 0x7FFFFFFFu));
+  }
+  return m;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t raw_max(const Raw<T>& r, uint32_t m) {
+  m = __vmaxu2(m, __vmaxu2(r.w[0].x & 0x7FFF7FFFu, r.w[0].y & 0x7FFF7FFFu));
+  return __vmaxu2(m, __vmaxu2(r.w[0].z & 0x7FFF7FFFu, r.w[0].w & 0x7FFF7FFFu));
+}
+
+// that maximum as a float32's bits
+template <typename T>
+__device__ __forceinline__ uint32_t max_bits(uint32_t m);
+template <>
+__device__ __forceinline__ uint32_t max_bits<float>(uint32_t m) { return m; }
+template <>
+__device__ __forceinline__ uint32_t max_bits<__nv_bfloat16>(uint32_t m) { return max(m << 16, m & 0xFFFF0000u); }
+template <>
+__device__ __forceinline__ uint32_t max_bits<__half>(uint32_t m) {
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)max(m & 0xFFFFu, m >> 16))));
+}
+
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
 }
 
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
@@ -87,7 +137,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
 __device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
@@ -97,10 +147,25 @@ __device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
     const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
 constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it leaves the nearest integer in the low bits
+
+// m / 127, correctly rounded: one Newton step on the product by 1/127 (checked
+// for every significand; subnormal results take the division)
+__device__ __forceinline__ float scale_of(float m) {
+  if (m < 0x1p-100f) return __fdiv_rn(m, 127.f);
+  constexpr float c = 1.f / 127.f;
+  const float q = m * c;
+  return fmaf(fmaf(-q, 127.f, m), c, q);
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // the code of x for scale s > 0: x / s to the nearest integer, ties to even
 __device__ __forceinline__ int exact_code(float x, float s, float guess) {
@@ -111,74 +176,82 @@ __device__ __forceinline__ int exact_code(float x, float s, float guess) {
   return (int)fminf(fmaxf(q, -127.f), 127.f);
 }
 
-// lanes: threads of a row (a power of two >= d / 8), so that a row never
-// crosses a warp; the lanes past d / 8 only take part in the shuffles
+// eight codes, one in the low byte of each word
+__device__ __forceinline__ void codes_of(const float (&v)[8], float s, uint32_t (&c)[8]) {
+  if (s >= 0x1p-80f) {
+    const float inv = rcp_approx(s);
+    float off = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float g = fmaf(v[e], inv, kMagic);
+      c[e] = __float_as_uint(g);
+      off = fmaxf(off, fabsf(fmaf(-(g - kMagic), s, v[e])));
+    }
+    // within just under half a step each: the guesses, off by 2^-15 of a step at
+    // most, cannot have crossed a border
+    if (off <= 0.4999f * s) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = (uint32_t)exact_code(v[e], s, rintf(v[e] * inv));
+  } else {
+    // 1/s would leave float32's range: the guess from both scaled up
+    const float inv = rcp_approx(s * 0x1p100f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = (uint32_t)exact_code(v[e], s, rintf(v[e] * 0x1p100f * inv));
+  }
+}
+
+// lanes: threads of a row (a power of two >= d / 16), so that a row never
+// crosses a warp; pieces past d / 8 only take part in the shuffles
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv8_write_kernel(Kv8Args a, int lanes) {
   const int which = blockIdx.y;
   const int sub = threadIdx.x & (lanes - 1);
   const int groups = kThreads / lanes;
-  const bool on = sub * 8 < a.d;
-  const T* x = static_cast<const T*>(a.x[which]);
+  const bool on[2] = {sub * 8 < a.d, (sub + lanes) * 8 < a.d};
+  const T* x = static_cast<const T*>(which ? a.x[1] : a.x[0]);
+  const int64_t x_stride = which ? a.x_stride[1] : a.x_stride[0];
+  int8_t* codes = which ? a.codes[1] : a.codes[0];
+  float* scales = which ? a.scales[1] : a.scales[0];
   const int64_t r0 = (int64_t)blockIdx.x * (groups * kRowsPerThread) + threadIdx.x / lanes;
-  float v[kRowsPerThread][8];
+  Raw<T> raw[kRowsPerThread][2];
   int64_t slot[kRowsPerThread];
 #pragma unroll
   for (int i = 0; i < kRowsPerThread; ++i) {
     const int64_t n = r0 + (int64_t)i * groups;
     slot[i] = -1;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+    raw[i][0] = raw[i][1] = zero_raw<T>();
     if (n < a.N) {
       slot[i] = __ldg(a.slots + n);
       const uint32_t t = (uint32_t)n / (uint32_t)a.Hkv, h = (uint32_t)n - t * (uint32_t)a.Hkv;
-      if (on) load8(x + (int64_t)t * a.x_stride[which] + (int64_t)h * a.d + sub * 8, v[i]);
+      const T* row = x + (int64_t)t * x_stride + (int64_t)h * a.d;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (on[k]) raw[i][k] = load_raw(row + (sub + k * lanes) * 8);
     }
   }
 #pragma unroll
   for (int i = 0; i < kRowsPerThread; ++i) {
-    // |x| ordered by its bits, so that an infinity or a NaN comes out on top
-    uint32_t mx = 0;
+    uint32_t top = max_bits<T>(raw_max(raw[i][1], raw_max(raw[i][0], 0u)));
+    for (int m = lanes >> 1; m; m >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+    const bool finite = top < 0x7F800000u;
+    const float s = finite ? scale_of(__uint_as_float(top)) : __uint_as_float(0x7FC00000u);
+    const bool kept = slot[i] >= 0 && slot[i] < a.rows;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) mx = max(mx, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
-    for (int m = lanes >> 1; m; m >>= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, m));
-    const bool finite = mx < 0x7F800000u;
-    const float s = finite ? __fdiv_rn(__uint_as_float(mx), 127.f) : __uint_as_float(0x7FC00000u);
-    uint32_t c[8];
-    if (!finite || s == 0.f) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) c[e] = 0;
-    } else if (s >= 0x1p-80f) {
-      const float inv = __frcp_rn(s);
-      bool near = false;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float g = fmaf(v[i][e], inv, kMagic);
-        c[e] = __float_as_uint(g);
-        const float r = fmaf(-(g - kMagic), s, v[i][e]);
-        // off by more than just under half a step: a tie, or the wrong side of one
-        near |= fabsf(r) > 0.4999f * s;
-      }
-      if (near) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = (uint32_t)exact_code(v[i][e], s, rintf(v[i][e] * inv));
-      }
-    } else {
-      // 1/s would leave float32's range: the guess from both scaled up
-      const float inv = __frcp_rn(s * 0x1p100f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) c[e] = (uint32_t)exact_code(v[i][e], s, rintf(v[i][e] * 0x1p100f * inv));
-    }
-    if (slot[i] >= 0 && slot[i] < a.rows) {
-      if (on) {
+    for (int k = 0; k < 2; ++k) {
+      float v[8];
+      uint32_t c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      floats_of(raw[i][k], v);
+      if (finite && s > 0.f) codes_of(v, s, c);
+      if (kept && on[k]) {
         uint2 w;
         w.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
         w.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
-        *reinterpret_cast<uint2*>(a.codes[which] + slot[i] * a.d + sub * 8) = w;
+        *reinterpret_cast<uint2*>(codes + slot[i] * a.d + (sub + k * lanes) * 8) = w;
       }
-      if (sub == 0) a.scales[which][slot[i]] = s;
-    } else if (slot[i] >= a.rows && sub == 0) {
-      atomicOr(a.status, kStatusRange);
+    }
+    if (sub == 0) {
+      if (kept) scales[slot[i]] = s;
+      else if (slot[i] >= a.rows) atomicOr(a.status, kStatusRange);
     }
   }
 }
@@ -188,11 +261,13 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(Kv8Args a, int lanes
   const int which = blockIdx.y;
   const int sub = threadIdx.x & (lanes - 1);
   const int groups = kThreads / lanes;
-  if (sub * 8 >= a.d) return;
-  T* out = static_cast<T*>(a.out[which]);
+  const bool on[2] = {sub * 8 < a.d, (sub + lanes) * 8 < a.d};
+  T* out = static_cast<T*>(which ? a.out[1] : a.out[0]);
+  const int8_t* codes = which ? a.codes[1] : a.codes[0];
+  const float* scales = which ? a.scales[1] : a.scales[0];
   const int64_t r0 = (int64_t)blockIdx.x * (groups * kRowsPerThread) + threadIdx.x / lanes;
   int64_t slot[kRowsPerThread];
-  uint2 w[kRowsPerThread];
+  uint2 w[kRowsPerThread][2];
   float s[kRowsPerThread];
 #pragma unroll
   for (int i = 0; i < kRowsPerThread; ++i) {
@@ -201,11 +276,14 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(Kv8Args a, int lanes
   }
 #pragma unroll
   for (int i = 0; i < kRowsPerThread; ++i) {
-    w[i] = make_uint2(0u, 0u);
+    w[i][0] = w[i][1] = make_uint2(0u, 0u);
     s[i] = 0.f;
     if (slot[i] >= 0 && slot[i] < a.rows) {
-      w[i] = __ldg(reinterpret_cast<const uint2*>(a.codes[which] + slot[i] * a.d + sub * 8));
-      s[i] = __ldg(a.scales[which] + slot[i]);
+      const int8_t* row = codes + slot[i] * a.d;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (on[k]) w[i][k] = __ldg(reinterpret_cast<const uint2*>(row + (sub + k * lanes) * 8));
+      s[i] = __ldg(scales + slot[i]);
     } else if (slot[i] >= a.rows && sub == 0) {
       atomicOr(a.status, kStatusRange);
     }
@@ -214,19 +292,24 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(Kv8Args a, int lanes
   for (int i = 0; i < kRowsPerThread; ++i) {
     const int64_t n = r0 + (int64_t)i * groups;
     if (n >= a.N) continue;
-    float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t word = e < 4 ? w[i].x : w[i].y;
-      v[e] = (float)(int8_t)(word >> (8 * (e & 3))) * s[i];
+    for (int k = 0; k < 2; ++k) {
+      if (!on[k]) continue;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // a code + 128 in the low byte of 2^23: the conversion is one subtraction
+        const uint32_t word = (e < 4 ? w[i][k].x : w[i][k].y) ^ 0x80808080u;
+        v[e] = (__uint_as_float(__byte_perm(word, 0x4B000000u, 0x7650u + (e & 3))) - 8388736.f) * s[i];
+      }
+      store8(out + n * a.d + (sub + k * lanes) * 8, v);
     }
-    store8(out + n * a.d + sub * 8, v);
   }
 }
 
 int lanes_of(int d) {
-  int l = 2;
-  while (l * 8 < d) l *= 2;
+  int l = 1;
+  while (l * 16 < d) l *= 2;
   return l;
 }
 
