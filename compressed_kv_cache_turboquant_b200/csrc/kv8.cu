@@ -16,7 +16,7 @@
 // Both directions are bound by HBM: d e + d + 4 bytes a row and tensor, plus 8
 // of the slot list (e: bytes of an element of x).  A thread takes two pieces of
 // eight elements, `lanes` pieces apart, so that neighbouring lanes read and
-// write neighbouring 16 (or 8) bytes, of each of four rows, whose loads are in
+// write neighbouring 16 (or 8) bytes, of each of two rows, whose loads are in
 // flight together; what a row needs once (its maximum, its scale, 1 / s) is
 // spread over sixteen elements.
 #include <cuda_bf16.h>
@@ -34,8 +34,8 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 256;
-constexpr int kRowsPerThread = 4;
+constexpr int kThreads = 128;
+constexpr int kRowsPerThread = 2;
 
 struct Kv8Args {
   const void* x[2];        // write: keys, values; read: unused
@@ -190,8 +190,15 @@ __device__ __forceinline__ void codes_of(const float (&v)[8], float s, uint32_t 
     // within just under half a step each: the guesses, off by 2^-15 of a step at
     // most, cannot have crossed a border
     if (off <= 0.4999f * s) return;
+    // 16-bit inputs meet exact ties often (x / s = 127 x / max, a ratio of small
+    // integers): one step towards the remainder r where |r| > s/2, or |r| = s/2
+    // and the code is odd, that is |r| > the float before s/2
+    const uint32_t half = __float_as_uint(0.5f * s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = (uint32_t)exact_code(v[e], s, rintf(v[e] * inv));
+    for (int e = 0; e < 8; ++e) {
+      const float r = fmaf(-(__uint_as_float(c[e]) - kMagic), s, v[e]);
+      if (fabsf(r) > __uint_as_float(half - (c[e] & 1u))) c[e] += 1u | (uint32_t)(__float_as_int(r) >> 31);
+    }
   } else {
     // 1/s would leave float32's range: the guess from both scaled up
     const float inv = rcp_approx(s * 0x1p100f);
