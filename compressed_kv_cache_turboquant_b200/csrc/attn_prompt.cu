@@ -17,12 +17,13 @@
 // CUDA cores, the tensor cores work for the other.  P is the inputs' type (one
 // rounding of 2^-9 or 2^-12 relative; l sums the unrounded weights).
 //
-// Warps (384 threads, one block per SM, persistent over the items):
-//   0-3, 4-7  softmax of row tile 0, 1: thread = row (TMEM lane); the reference
-//             moves, and O is rescaled, only when a logit passes it by 2^8
-//   8         TMA: the item's Q tiles, then K and V tiles through a ring
-//   9         the single-thread MMA issuer
-//   10, 11    look through the V tiles that some row does not see whole: an
+// Warps (640 threads, one block per SM, persistent over the items):
+//   0-7, 8-15 softmax of row tile 0, 1: two threads a row (TMEM lane), 64 keys
+//             of a tile each, that exchange their maxima; the reference moves,
+//             and O is rescaled, only when a logit passes it by 2^8
+//   16        TMA: the item's Q tiles, then K and V tiles through a ring
+//   17        the MMA issuer
+//   18, 19    look through the V tiles that some row does not see whole: an
 //             infinity or NaN there, times a weight of 0, would spoil rows that
 //             must not see it.  Such elements become 0 in shared memory, and the
 //             rows that do see them add them at the end (a bit per key)
@@ -47,8 +48,8 @@ namespace {
 using namespace sm100;
 
 constexpr int kTile = 128;                 // rows of a row tile, keys of a key tile
-constexpr int kThreads = 384;
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;   // 2 x 208 + 88 = 3 x 168, the registers at launch
+constexpr int kThreads = 640;
+constexpr int kRegsSoftmax = 104, kRegsOther = 64;   // 4 x 104 + 64 = 5 x 96, the registers at launch
 constexpr uint32_t kColS = 0, kColO = 256; // S/P of tiles 0, 1 at 0, 128; O at 256, 384
 constexpr float kLazy = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -56,6 +57,11 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kBadSlots = 8;               // items whose bad-key bits are kept (more than the ring can run ahead)
 constexpr int kBadTiles = 4;               // key tiles of an item that some row does not see whole: 3 at most
 constexpr int kBuckets = 1024;
+constexpr int kPolyPairs = 0;              // pairs of every four whose 2^x is a polynomial
+// 2^f on [-1/2, 1/2], least relative error at degree 5 (7.5e-8 before rounding
+// to float32), fitted by reweighted least squares on Chebyshev points
+constexpr float kPoly0 = 1.0000001f, kPoly1 = 0.69314694f, kPoly2 = 0.2402212f, kPoly3 = 0.05550713f,
+                kPoly4 = 0.009675542f, kPoly5 = 0.0013276471f;
 
 template <int D>
 struct Shape {
@@ -64,8 +70,9 @@ struct Shape {
   static constexpr int stages = D == 128 ? 4 : 8;
   static constexpr int off_ring = 2 * tile;
   static constexpr int off_bad = off_ring + stages * tile;   // [kBadSlots][1 + 4 kBadTiles] words
-  static constexpr int off_bar = off_bad + kBadSlots * (1 + 4 * kBadTiles) * 4;
-  static constexpr int bytes = (off_bar + 320 + 16 + 1023) / 1024 * 1024 + 1024;
+  static constexpr int off_swap = off_bad + kBadSlots * (1 + 4 * kBadTiles) * 4;   // [2][2 tiles][2 halves][128]
+  static constexpr int off_bar = off_swap + 2 * 4 * kTile * 4;
+  static constexpr int bytes = (off_bar + 384 + 1023) / 1024 * 1024 + 1024;
 };
 
 struct PromptArgs {
@@ -108,27 +115,97 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t l
   return d;
 }
 
+// The issuing warp runs its loop as a whole, so that descriptors and addresses
+// stay in uniform registers (a loop of one thread moves each operand there one
+// by one: 130 cycles a product instead of the 64 it takes); `lead` is set in
+// the lane whose instructions count.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t lead;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(lead));
+  return lead;
+}
+
+// D (+)= A B^T, both from shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+
+// A from tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
+      ::"r"(smem_u32(bar)), "r"(lead)
+      : "memory");
+}
+
 // keeps every use of registers that tcgen05.ld fills behind its wait
 __device__ __forceinline__ void regs_after_wait(float (&r)[32]) {
   asm volatile(""
                : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])::"memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
+// the largest, or NaN where one of them is
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// two float32 in one 64-bit register: sm_100 multiplies and adds them as a pair
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// 2^x of a pair on the FMA pipe, x <= 2^7: 2^n by the exponent field, 2^f for
+// f in [-1/2, 1/2] by the polynomial of degree 5 with the least relative error
+// (2.0e-7 with float32 coefficients; the hardware's 2^x has 1.2e-7).  Below
+// -126 the result stays near 2^-126.
+__device__ __forceinline__ uint64_t ex2_poly(uint64_t x2) {
+  float x, y;
+  unpair(x2, x, y);
+  x2 = pair(fmaxf(x, -126.f), fmaxf(y, -126.f));
+  const uint64_t t = add2(x2, pair(12582912.f, 12582912.f));        // + 1.5 2^23: n in the low bits
+  const uint64_t n = add2(t, pair(-12582912.f, -12582912.f));
+  const uint64_t f = fma2(n, pair(-1.f, -1.f), x2);
+  uint64_t p = pair(kPoly5, kPoly5);
+  p = fma2(p, f, pair(kPoly4, kPoly4));
+  p = fma2(p, f, pair(kPoly3, kPoly3));
+  p = fma2(p, f, pair(kPoly2, kPoly2));
+  p = fma2(p, f, pair(kPoly1, kPoly1));
+  p = fma2(p, f, pair(kPoly0, kPoly0));
+  float px, py, tx, ty;
+  unpair(p, px, py);
+  unpair(t, tx, ty);
+  return pair(__uint_as_float(__float_as_uint(px) + (__float_as_uint(tx) << 23)),
+              __uint_as_float(__float_as_uint(py) + (__float_as_uint(ty) << 23)));
 }
 
 __device__ __forceinline__ uint32_t pack(float lo, float hi, __nv_bfloat16) {
@@ -262,13 +339,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   uint64_t* q_free = q_full + 1;         // MMA commit: the item's logit products are done
   uint64_t* clean = q_free + 1;          // [stages] both scanning warps: looked through, where it needs that
   uint64_t* s_full = clean + S::stages;       // [2] MMA commit: logits of a tile
-  uint64_t* p_ready = s_full + 2;        // [2] 4 softmax warps: weights written
-  uint64_t* pv_done = p_ready + 2;       // [2] MMA commit: value product done
+  uint64_t* p_ready = s_full + 2;        // [2][2] 4 softmax warps: weights of a tile's first, second 64 keys written
+  uint64_t* pv_done = p_ready + 4;       // [2] MMA commit: value product done
   uint64_t* done = pv_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   int4* direct_item = reinterpret_cast<int4*>(smem + S::off_bar + 320);
+  volatile int* dead = reinterpret_cast<int*>(smem + S::off_bar + 336);   // [8] pairs of softmax warps: a wait ran out
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::stages; ++s) {
       mbar_init(&full[s], 1);
@@ -279,13 +357,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
     mbar_init(q_free, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_ready[t], 4);
+      mbar_init(&p_ready[2 * t], 4);
+      mbar_init(&p_ready[2 * t + 1], 4);
       mbar_init(&pv_done[t], 1);
     }
     mbar_init(done, 1);
+    for (int x = 0; x < 8; ++x) dead[x] = 0;
     fence_mbar_init();
   }
-  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  if (warp == 17) tmem_alloc(tmem_slot, 512);
   if (a.direct && warp == 0) {
     // the sequence of item blockIdx.x / Hkv, with the plan's reading of the bounds
     int left = blockIdx.x / a.Hkv, prev = min(max(__ldg(a.cu), 0), a.total);
@@ -353,9 +433,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   auto first_cut = [&](const Item& it) { return (it.tok[0] + 1) / kTile; };
   Item it;
 
-  if (warp >= 8) {
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 8) {
+    if (warp == 16) {
       // ---------------- TMA
       if (lane == 0) {
         int st = 0;
@@ -386,71 +466,75 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         for (int x = st > S::stages ? st - S::stages : 0; x < st; ++x)
           if (!mbar_wait(&full[x % S::stages], (uint32_t)((x / S::stages) & 1))) atomicOr(a.status, kStatusTimeout);
       }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
       // ---------------- MMA
-      if (lane == 0) {
-        constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-        const uint32_t idesc_s = idesc_f16(kTile, kTile, bf), idesc_o = idesc_f16(kTile, D, bf) | (1u << 16);
-        const uint32_t qb = smem_u32(smem), rb = smem_u32(ring);
-        int st = 0, pv[2] = {0, 0};
-        bool ok = true;
-        auto wait_full = [&](int x) { return mbar_wait(&full[x % S::stages], (uint32_t)((x / S::stages) & 1)); };
-        // S of tile t from the K tile of ring step x; the buffer's last P must have been consumed
-        auto logits = [&](int t, int x) -> bool {
-          if (pv[t] > 0 && !mbar_wait(&pv_done[t], (uint32_t)((pv[t] - 1) & 1))) return false;
-          tc_fence_after();
-          const uint32_t kb = rb + (x % S::stages) * S::tile, q = qb + t * S::tile;
+      constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+      constexpr uint32_t idesc_s = idesc_f16(kTile, kTile, bf), idesc_o = idesc_f16(kTile, D, bf) | (1u << 16);
+      const uint32_t lead = elect_one();
+      const uint64_t qd = sw128_kmajor_desc(smem_u32(smem)), kd = sw128_kmajor_desc(smem_u32(ring));
+      const uint64_t vd = sw128_mnmajor_desc(smem_u32(ring), kTile * 128);
+      int st = 0, pv0 = 0, pv1 = 0;                         // ring steps; value products of tiles 0, 1 so far
+      bool ok = true;
+      auto wait_full = [&](int x) { return mbar_wait_warp(&full[x % S::stages], (uint32_t)((x / S::stages) & 1)); };
+      // S of tile t from the K tile of ring step x; the buffer's last P must have been consumed
+      auto logits = [&](int t, int pv, int x) -> bool {
+        if (pv > 0 && !mbar_wait_warp(&pv_done[t], (uint32_t)((pv - 1) & 1))) return false;
+        tc_fence_after();
+        const uint64_t q = qd + t * (S::tile >> 4), k = kd + (uint32_t)(x % S::stages) * (S::tile >> 4);
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (uint32_t)((ks >> 2) * kTile * 128 + (ks & 3) * 32);
-            mma_f16(tmem + kColS + t * 128, sw128_kmajor_desc(q + off), sw128_kmajor_desc(kb + off), idesc_s, ks ? 1u : 0u);
-          }
-          mma_commit(&s_full[t]);
-          return true;
-        };
-        auto values = [&](int t, int x, bool first) -> bool {
-          if (!mbar_wait(&p_ready[t], (uint32_t)(pv[t] & 1))) return false;
-          tc_fence_after();
-          const uint32_t vb = rb + (x % S::stages) * S::tile;
-#pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            mma_f16_ta(tmem + kColO + t * 128, tmem + kColS + t * 128 + 8 * ks, sw128_mnmajor_desc(vb + ks * 2048, kTile * 128),
-                       idesc_o, (first && ks == 0) ? 0u : 1u);
-          mma_commit(&pv_done[t]);
-          ++pv[t];
-          return true;
-        };
-        for (int i = 0; ok && item(i, it); ++i) {
-          ok = mbar_wait(q_full, (uint32_t)(i & 1)) && wait_full(st) && (!it.n[0] || logits(0, st)) && (!it.n[1] || logits(1, st));
-          if (!ok) break;
-          mma_commit(&empty[st % S::stages]);
-          if (it.tiles == 1) mma_commit(q_free);
-          const int cut = first_cut(it);
-          for (int j = 0; j < it.tiles; ++j) {
-            const int xv = st + 2 * j + 1, xk = xv + 1;
-            // a tile that some row does not see whole has to be looked through first
-            ok = wait_full(xv) && (j < cut || mbar_wait(&clean[xv % S::stages], (uint32_t)((xv / S::stages) & 1)));
-            if (!ok) break;
-            const bool more = j + 1 < it.tiles;
-            if (j < it.n[0] && !(ok = values(0, xv, j == 0))) break;
-            if (more && !(ok = wait_full(xk))) break;
-            if (j + 1 < it.n[0] && !(ok = logits(0, xk))) break;
-            if (j < it.n[1] && !(ok = values(1, xv, j == 0))) break;
-            mma_commit(&empty[xv % S::stages]);
-            if (j + 1 < it.n[1] && !(ok = logits(1, xk))) break;
-            if (more) mma_commit(&empty[xk % S::stages]);
-            if (j + 2 == it.tiles) mma_commit(q_free);
-          }
-          st += 2 * it.tiles;
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (uint32_t)((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4;
+          mma_ss(tmem + kColS + t * 128, q + off, k + off, idesc_s, ks ? 1u : 0u, lead);
         }
-        if (!ok) atomicOr(a.status, kStatusTimeout);
-        // nothing may still run when tensor memory is given back
-        mma_commit(done);
-        if (!mbar_wait(done, 0)) atomicOr(a.status, kStatusTimeout);
+        commit(&s_full[t], lead);
+        return true;
+      };
+      auto values = [&](int t, int pv, int x, bool first) -> bool {
+        const uint64_t v = vd + (uint32_t)(x % S::stages) * (S::tile >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kTile / 16; ++ks) {
+          // the weights come in two halves, of a warp each
+          if (ks % (kTile / 32) == 0) {
+            if (!mbar_wait_warp(&p_ready[2 * t + ks / (kTile / 32)], (uint32_t)(pv & 1))) return false;
+            tc_fence_after();
+          }
+          mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + 8 * ks, v + ks * (2048 >> 4), idesc_o,
+                 (first && ks == 0) ? 0u : 1u, lead);
+        }
+        commit(&pv_done[t], lead);
+        return true;
+      };
+      for (int i = 0; ok && item(i, it); ++i) {
+        ok = mbar_wait_warp(q_full, (uint32_t)(i & 1)) && wait_full(st) && (!it.n[0] || logits(0, pv0, st)) &&
+             (!it.n[1] || logits(1, pv1, st));
+        if (!ok) break;
+        commit(&empty[st % S::stages], lead);
+        if (it.tiles == 1) commit(q_free, lead);
+        const int cut = first_cut(it);
+        for (int j = 0; j < it.tiles; ++j) {
+          const int xv = st + 2 * j + 1, xk = xv + 1;
+          // a tile that some row does not see whole has to be looked through first
+          ok = wait_full(xv) && (j < cut || mbar_wait_warp(&clean[xv % S::stages], (uint32_t)((xv / S::stages) & 1)));
+          if (!ok) break;
+          const bool more = j + 1 < it.tiles;
+          if (j < it.n[0] && !(ok = values(0, pv0++, xv, j == 0))) break;
+          if (more && !(ok = wait_full(xk))) break;
+          if (j + 1 < it.n[0] && !(ok = logits(0, pv0, xk))) break;
+          if (j < it.n[1] && !(ok = values(1, pv1++, xv, j == 0))) break;
+          commit(&empty[xv % S::stages], lead);
+          if (j + 1 < it.n[1] && !(ok = logits(1, pv1, xk))) break;
+          if (more) commit(&empty[xk % S::stages], lead);
+          if (j + 2 == it.tiles) commit(q_free, lead);
+        }
+        st += 2 * it.tiles;
       }
+      if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
+      // nothing may still run when tensor memory is given back
+      commit(done, lead);
+      if (!mbar_wait_warp(done, 0) && lane == 0) atomicOr(a.status, kStatusTimeout);
     } else {
       // ---------------- V tiles that some row does not see whole
-      const int w = warp - 10;
+      const int w = warp - 18;
       int st = 0;
       bool ok = true;
       for (int i = 0; ok && item(i, it); ++i) {
@@ -497,46 +581,65 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
     }
   } else {
-    // ---------------- softmax: thread = row of tile t
+    // ---------------- softmax: thread = row of tile t, keys hf * 64 .. of a key tile
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int t = warp >> 2, r = threadIdx.x & 127;
+    const int t = warp >> 3, hf = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
+    const int couple = t * 4 + (warp & 3);                  // the two warps of 32 rows
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t sc = tmem + lanes + kColS + t * 128, oc = tmem + lanes + kColO + t * 128;
+    const uint32_t sc = tmem + lanes + kColS + t * 128, oc = tmem + lanes + kColO + t * 128 + hf * (D / 2);
+    float* swap = reinterpret_cast<float*>(smem + S::off_swap) + t * 2 * kTile + r;
     const int row_tok = r / a.G, row_head = r % a.G;
     const float cl = a.scale_log2;
-    int steps = 0;
+    int steps = 0, turn = 0;
     bool ok = true;
-    for (int i = 0; ok && item(i, it); ++i) {
+    // what the other thread of the row has; both threads call it together
+    auto exchange = [&](float mine) -> float {
+      float* at = swap + (turn++ & 1) * 4 * kTile;
+      at[hf * kTile] = mine;
+      named_bar_sync(1 + couple, 64);
+      return at[(hf ^ 1) * kTile];
+    };
+    bool go = true;
+    for (int i = 0; go && item(i, it); ++i) {
       const int n = it.n[t];
       if (n == 0) continue;
       const int pos = it.tok[t] + row_tok;                  // the row's token in its sequence
       const bool live = row_tok < a.tq && pos < it.len;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++steps) {
-        if (!(ok = mbar_wait_warp(&s_full[t], (uint32_t)(steps & 1)))) break;
+        if (ok) ok = mbar_wait_warp(&s_full[t], (uint32_t)(steps & 1));
+        if (!ok) dead[couple] = 1;                          // the other warp leaves with this one, at the exchange
         tc_fence_after();
-        float x[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(sc + 32 * c, x[c]);
+        float x[2][32];
+        tmem_ld32(sc + 64 * hf, x[0]);
+        tmem_ld32(sc + 64 * hf + 32, x[1]);
         tmem_wait_ld();
+        regs_after_wait(x[0]);
+        regs_after_wait(x[1]);
+        const int lim = pos - j * kTile - hf * 64;          // keys past it take no part
+        if (__any_sync(kFull, lim < 63)) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) regs_after_wait(x[c]);
-        const int lim = pos - j * kTile;                    // keys past it take no part
-        if (__any_sync(kFull, lim < kTile - 1)) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[c][e] = 32 * c + e <= lim ? x[c][e] : -INFINITY;
         }
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          mx[c] = max3(x[c][0], x[c][1], x[c][2]);
+          const float* y = x[c >> 1] + 16 * (c & 1);
+          mx[c] = max3(y[0], y[1], y[2]);
 #pragma unroll
-          for (int e = 3; e + 1 < 32; e += 2) mx[c] = max3(mx[c], x[c][e], x[c][e + 1]);
-          mx[c] = fmaxf(mx[c], x[c][31]);
+          for (int e = 3; e + 1 < 16; e += 2) mx[c] = max3(mx[c], y[e], y[e + 1]);
+          mx[c] = max3(mx[c], y[15], y[15]);
         }
-        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * cl;
+        const float own = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+        const float other = exchange(own);
+        if (dead[couple]) {
+          go = false;
+          break;
+        }
+        const float top = max3(own, other, other) * cl;
+        if (!(top < INFINITY)) l = NAN;                     // a seen logit is NaN or infinite: so is the row
         const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
         if (__any_sync(kFull, grow)) {
           float f = 1.f;
@@ -546,43 +649,62 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
             m = top;
           }
           if (j > 0) {
-            // the value product of tile j - 1 was done before this tile's logits began
+            // the value product of tile j - 1 was done before this tile's logits
+            // began; each thread rescales half the columns, and neither goes on
+            // to its weights before the other is done
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              tmem_ld32(oc + 32 * c, o);
+            for (int c = 0; c < D / 2; c += 16) {
+              float o[16];
+              tmem_ld16(oc + c, o);
               tmem_wait_ld();
-              regs_after_wait(o);
-              uint32_t u[32];
+              uint32_t u[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(f == 0.f ? 0.f : o[e] * f);
-              tmem_st32(oc + 32 * c, u);
+              for (int e = 0; e < 16; ++e) {
+                asm volatile("" : "+f"(o[e])::"memory");
+                u[e] = __float_as_uint(f == 0.f ? 0.f : o[e] * f);
+              }
+              tmem_st16(oc + c, u);
             }
+            tmem_wait_st();
+            tc_fence_before();
+            named_bar_sync(1 + couple, 64);
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t cl2 = pair(cl, cl), ref2 = pair(-ref, -ref);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t u[32];
+        for (int c = 0; c < 2; ++c) {
+          uint32_t u[16];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float p0 = ex2(fmaf(x[2 * hf + c][e], cl, -ref)), p1 = ex2(fmaf(x[2 * hf + c][e + 1], cl, -ref));
-              sum[(e >> 1) & 3] += p0 + p1;
-              u[16 * c + e / 2] = pack(p0, p1, T());
+          for (int e = 0; e < 16; ++e) {
+            uint64_t z = fma2(pair(x[c][2 * e], x[c][2 * e + 1]), cl2, ref2);
+            float p0, p1;
+            if (e % 4 < kPolyPairs) {
+              z = ex2_poly(z);
+              unpair(z, p0, p1);
+            } else {
+              unpair(z, p0, p1);
+              p0 = ex2(p0), p1 = ex2(p1);
+              z = pair(p0, p1);
             }
-          tmem_st32(sc + 32 * hf, u);
+            sum[e & 1] = add2(sum[e & 1], z);
+            u[e] = pack(p0, p1, T());
+          }
+          tmem_st16(sc + 32 * hf + 16 * c, u);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float s0, s1;
+        unpair(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[t]);
+        if (lane == 0) mbar_arrive(&p_ready[2 * t + hf]);
       }
-      if (!ok) break;
-      if (!(ok = mbar_wait_warp(&pv_done[t], (uint32_t)((steps - 1) & 1)))) break;
+      if (!go) break;
+      l += exchange(l);
+      if (ok) ok = mbar_wait_warp(&pv_done[t], (uint32_t)((steps - 1) & 1));
+      if (!ok) continue;                                    // the next exchange ends both warps
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t row = (int64_t)(it.start + pos) * a.Hq + it.h * a.G + row_head;
@@ -592,11 +714,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       uint32_t some = 0;
       for (int x = 0; x < (it.tiles - cut) * 4; ++x) some |= bits[x];
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < D / 2; c += 32) {
         float o[32];
-        tmem_ld32(oc + 32 * c, o);
+        tmem_ld32(oc + c, o);
         tmem_wait_ld();
         regs_after_wait(o);
+        const int col = hf * (D / 2) + c;
         if (some) {
           // infinities and NaN that the row does see, taken out of the V tiles above
           for (int x = 0; x < (it.tiles - cut) * 4; ++x)
@@ -606,7 +729,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
               const T* v = static_cast<const T*>(a.v) + (int64_t)(it.start + key) * a.v_stride + (int64_t)it.h * a.d;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const float y = 32 * c + e < a.d ? (float)v[32 * c + e] : 0.f;
+                const float y = col + e < a.d ? (float)v[col + e] : 0.f;
                 if (!(fabsf(y) < INFINITY)) o[e] += y;
               }
             }
@@ -614,17 +737,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         if (live) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
-            if (32 * c + e < a.d) {
+            if (col + e < a.d) {
               uint4 w;
               w.x = pack(o[e] * inv, o[e + 1] * inv, T());
               w.y = pack(o[e + 2] * inv, o[e + 3] * inv, T());
               w.z = pack(o[e + 4] * inv, o[e + 5] * inv, T());
               w.w = pack(o[e + 6] * inv, o[e + 7] * inv, T());
-              *reinterpret_cast<uint4*>(out + 32 * c + e) = w;
+              *reinterpret_cast<uint4*>(out + col + e) = w;
             }
         }
       }
-      if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      if (live && a.lse && hf == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       tc_fence_before();
     }
     if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
@@ -633,7 +756,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 // [tokens][heads][d] with a token stride, as boxes of 64 coordinates x `heads`
