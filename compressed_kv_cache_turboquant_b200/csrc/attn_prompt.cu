@@ -17,13 +17,12 @@
 // CUDA cores, the tensor cores work for the other.  P is the inputs' type (one
 // rounding of 2^-9 or 2^-12 relative; l sums the unrounded weights).
 //
-// Warps (640 threads, one block per SM, persistent over the items):
-//   0-7, 8-15 softmax of row tile 0, 1: two threads a row (TMEM lane), 64 keys
-//             of a tile each, that exchange their maxima; the reference moves,
-//             and O is rescaled, only when a logit passes it by 2^8
-//   16        TMA: the item's Q tiles, then K and V tiles through a ring
-//   17        the MMA issuer
-//   18, 19    look through the V tiles that some row does not see whole: an
+// Warps (384 threads, one block per SM, persistent over the items):
+//   0-3, 4-7  softmax of row tile 0, 1: thread = row (TMEM lane); the reference
+//             moves, and O is rescaled, only when a logit passes it by 2^8
+//   8         TMA: the item's Q tiles, then K and V tiles through a ring
+//   9         the MMA issuer
+//   10, 11    look through the V tiles that some row does not see whole: an
 //             infinity or NaN there, times a weight of 0, would spoil rows that
 //             must not see it.  Such elements become 0 in shared memory, and the
 //             rows that do see them add them at the end (a bit per key)
@@ -48,8 +47,8 @@ namespace {
 using namespace sm100;
 
 constexpr int kTile = 128;                 // rows of a row tile, keys of a key tile
-constexpr int kThreads = 640;
-constexpr int kRegsSoftmax = 104, kRegsOther = 64;   // 4 x 104 + 64 = 5 x 96, the registers at launch
+constexpr int kThreads = 384;
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;   // 2 x 208 + 88 = 3 x 168, the registers at launch
 constexpr uint32_t kColS = 0, kColO = 256; // S/P of tiles 0, 1 at 0, 128; O at 256, 384
 constexpr float kLazy = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -57,11 +56,6 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kBadSlots = 8;               // items whose bad-key bits are kept (more than the ring can run ahead)
 constexpr int kBadTiles = 4;               // key tiles of an item that some row does not see whole: 3 at most
 constexpr int kBuckets = 1024;
-constexpr int kPolyPairs = 0;              // pairs of every four whose 2^x is a polynomial
-// 2^f on [-1/2, 1/2], least relative error at degree 5 (7.5e-8 before rounding
-// to float32), fitted by reweighted least squares on Chebyshev points
-constexpr float kPoly0 = 1.0000001f, kPoly1 = 0.69314694f, kPoly2 = 0.2402212f, kPoly3 = 0.05550713f,
-                kPoly4 = 0.009675542f, kPoly5 = 0.0013276471f;
 
 template <int D>
 struct Shape {
@@ -70,8 +64,7 @@ struct Shape {
   static constexpr int stages = D == 128 ? 4 : 8;
   static constexpr int off_ring = 2 * tile;
   static constexpr int off_bad = off_ring + stages * tile;   // [kBadSlots][1 + 4 kBadTiles] words
-  static constexpr int off_swap = off_bad + kBadSlots * (1 + 4 * kBadTiles) * 4;   // [2][2 tiles][2 halves][128]
-  static constexpr int off_bar = off_swap + 2 * 4 * kTile * 4;
+  static constexpr int off_bar = off_bad + kBadSlots * (1 + 4 * kBadTiles) * 4;
   static constexpr int bytes = (off_bar + 384 + 1023) / 1024 * 1024 + 1024;
 };
 
@@ -182,30 +175,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
-}
-
-// 2^x of a pair on the FMA pipe, x <= 2^7: 2^n by the exponent field, 2^f for
-// f in [-1/2, 1/2] by the polynomial of degree 5 with the least relative error
-// (2.0e-7 with float32 coefficients; the hardware's 2^x has 1.2e-7).  Below
-// -126 the result stays near 2^-126.
-__device__ __forceinline__ uint64_t ex2_poly(uint64_t x2) {
-  float x, y;
-  unpair(x2, x, y);
-  x2 = pair(fmaxf(x, -126.f), fmaxf(y, -126.f));
-  const uint64_t t = add2(x2, pair(12582912.f, 12582912.f));        // + 1.5 2^23: n in the low bits
-  const uint64_t n = add2(t, pair(-12582912.f, -12582912.f));
-  const uint64_t f = fma2(n, pair(-1.f, -1.f), x2);
-  uint64_t p = pair(kPoly5, kPoly5);
-  p = fma2(p, f, pair(kPoly4, kPoly4));
-  p = fma2(p, f, pair(kPoly3, kPoly3));
-  p = fma2(p, f, pair(kPoly2, kPoly2));
-  p = fma2(p, f, pair(kPoly1, kPoly1));
-  p = fma2(p, f, pair(kPoly0, kPoly0));
-  float px, py, tx, ty;
-  unpair(p, px, py);
-  unpair(t, tx, ty);
-  return pair(__uint_as_float(__float_as_uint(px) + (__float_as_uint(tx) << 23)),
-              __uint_as_float(__float_as_uint(py) + (__float_as_uint(ty) << 23)));
 }
 
 __device__ __forceinline__ uint32_t pack(float lo, float hi, __nv_bfloat16) {
@@ -344,7 +313,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   uint64_t* done = pv_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   int4* direct_item = reinterpret_cast<int4*>(smem + S::off_bar + 320);
-  volatile int* dead = reinterpret_cast<int*>(smem + S::off_bar + 336);   // [8] pairs of softmax warps: a wait ran out
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -362,10 +330,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       mbar_init(&pv_done[t], 1);
     }
     mbar_init(done, 1);
-    for (int x = 0; x < 8; ++x) dead[x] = 0;
     fence_mbar_init();
   }
-  if (warp == 17) tmem_alloc(tmem_slot, 512);
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
   if (a.direct && warp == 0) {
     // the sequence of item blockIdx.x / Hkv, with the plan's reading of the bounds
     int left = blockIdx.x / a.Hkv, prev = min(max(__ldg(a.cu), 0), a.total);
@@ -433,9 +400,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   auto first_cut = [&](const Item& it) { return (it.tok[0] + 1) / kTile; };
   Item it;
 
-  if (warp >= 16) {
+  if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 16) {
+    if (warp == 8) {
       // ---------------- TMA
       if (lane == 0) {
         int st = 0;
@@ -466,7 +433,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         for (int x = st > S::stages ? st - S::stages : 0; x < st; ++x)
           if (!mbar_wait(&full[x % S::stages], (uint32_t)((x / S::stages) & 1))) atomicOr(a.status, kStatusTimeout);
       }
-    } else if (warp == 17) {
+    } else if (warp == 9) {
       // ---------------- MMA
       constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
       constexpr uint32_t idesc_s = idesc_f16(kTile, kTile, bf), idesc_o = idesc_f16(kTile, D, bf) | (1u << 16);
@@ -493,7 +460,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         const uint64_t v = vd + (uint32_t)(x % S::stages) * (S::tile >> 4);
 #pragma unroll
         for (int ks = 0; ks < kTile / 16; ++ks) {
-          // the weights come in two halves, of a warp each
+          // the weights come in two halves
           if (ks % (kTile / 32) == 0) {
             if (!mbar_wait_warp(&p_ready[2 * t + ks / (kTile / 32)], (uint32_t)(pv & 1))) return false;
             tc_fence_after();
@@ -534,7 +501,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       if (!mbar_wait_warp(done, 0) && lane == 0) atomicOr(a.status, kStatusTimeout);
     } else {
       // ---------------- V tiles that some row does not see whole
-      const int w = warp - 18;
+      const int w = warp - 10;
       int st = 0;
       bool ok = true;
       for (int i = 0; ok && item(i, it); ++i) {
@@ -581,64 +548,46 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
     }
   } else {
-    // ---------------- softmax: thread = row of tile t, keys hf * 64 .. of a key tile
+    // ---------------- softmax: thread = row of tile t
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int t = warp >> 3, hf = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
-    const int couple = t * 4 + (warp & 3);                  // the two warps of 32 rows
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t sc = tmem + lanes + kColS + t * 128, oc = tmem + lanes + kColO + t * 128 + hf * (D / 2);
-    float* swap = reinterpret_cast<float*>(smem + S::off_swap) + t * 2 * kTile + r;
+    const uint32_t sc = tmem + lanes + kColS + t * 128, oc = tmem + lanes + kColO + t * 128;
     const int row_tok = r / a.G, row_head = r % a.G;
     const float cl = a.scale_log2;
-    int steps = 0, turn = 0;
+    int steps = 0;
     bool ok = true;
-    // what the other thread of the row has; both threads call it together
-    auto exchange = [&](float mine) -> float {
-      float* at = swap + (turn++ & 1) * 4 * kTile;
-      at[hf * kTile] = mine;
-      named_bar_sync(1 + couple, 64);
-      return at[(hf ^ 1) * kTile];
-    };
-    bool go = true;
-    for (int i = 0; go && item(i, it); ++i) {
+    for (int i = 0; ok && item(i, it); ++i) {
       const int n = it.n[t];
       if (n == 0) continue;
       const int pos = it.tok[t] + row_tok;                  // the row's token in its sequence
       const bool live = row_tok < a.tq && pos < it.len;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++steps) {
-        if (ok) ok = mbar_wait_warp(&s_full[t], (uint32_t)(steps & 1));
-        if (!ok) dead[couple] = 1;                          // the other warp leaves with this one, at the exchange
+        if (!(ok = mbar_wait_warp(&s_full[t], (uint32_t)(steps & 1)))) break;
         tc_fence_after();
-        float x[2][32];
-        tmem_ld32(sc + 64 * hf, x[0]);
-        tmem_ld32(sc + 64 * hf + 32, x[1]);
-        tmem_wait_ld();
-        regs_after_wait(x[0]);
-        regs_after_wait(x[1]);
-        const int lim = pos - j * kTile - hf * 64;          // keys past it take no part
-        if (__any_sync(kFull, lim < 63)) {
+        float x[4][32];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 4; ++c) tmem_ld32(sc + 32 * c, x[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) regs_after_wait(x[c]);
+        const int lim = pos - j * kTile;                    // keys past it take no part
+        if (__any_sync(kFull, lim < kTile - 1)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[c][e] = 32 * c + e <= lim ? x[c][e] : -INFINITY;
         }
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float* y = x[c >> 1] + 16 * (c & 1);
-          mx[c] = max3(y[0], y[1], y[2]);
+          mx[c] = max3(x[c][0], x[c][1], x[c][2]);
 #pragma unroll
-          for (int e = 3; e + 1 < 16; e += 2) mx[c] = max3(mx[c], y[e], y[e + 1]);
-          mx[c] = max3(mx[c], y[15], y[15]);
+          for (int e = 3; e + 1 < 32; e += 2) mx[c] = max3(mx[c], x[c][e], x[c][e + 1]);
+          mx[c] = max3(mx[c], x[c][31], x[c][31]);
         }
-        const float own = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
-        const float other = exchange(own);
-        if (dead[couple]) {
-          go = false;
-          break;
-        }
-        const float top = max3(own, other, other) * cl;
+        const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * cl;
         if (!(top < INFINITY)) l = NAN;                     // a seen logit is NaN or infinite: so is the row
         const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
         if (__any_sync(kFull, grow)) {
@@ -649,11 +598,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
             m = top;
           }
           if (j > 0) {
-            // the value product of tile j - 1 was done before this tile's logits
-            // began; each thread rescales half the columns, and neither goes on
-            // to its weights before the other is done
+            // the value product of tile j - 1 was done before this tile's logits began
 #pragma unroll 1
-            for (int c = 0; c < D / 2; c += 16) {
+            for (int c = 0; c < D; c += 16) {
               float o[16];
               tmem_ld16(oc + c, o);
               tmem_wait_ld();
@@ -665,46 +612,39 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
               }
               tmem_st16(oc + c, u);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            named_bar_sync(1 + couple, 64);
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
         const uint64_t cl2 = pair(cl, cl), ref2 = pair(-ref, -ref);
         uint64_t sum[2] = {0, 0};
+        // half the keys at a time: the value product of the first half runs during the second
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t u[16];
+        for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            uint64_t z = fma2(pair(x[c][2 * e], x[c][2 * e + 1]), cl2, ref2);
-            float p0, p1;
-            if (e % 4 < kPolyPairs) {
-              z = ex2_poly(z);
-              unpair(z, p0, p1);
-            } else {
+          for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
+            uint32_t u[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              uint64_t z = fma2(pair(x[c][2 * e], x[c][2 * e + 1]), cl2, ref2);
+              float p0, p1;
               unpair(z, p0, p1);
               p0 = ex2(p0), p1 = ex2(p1);
-              z = pair(p0, p1);
+              sum[e & 1] = add2(sum[e & 1], pair(p0, p1));
+              u[e] = pack(p0, p1, T());
             }
-            sum[e & 1] = add2(sum[e & 1], z);
-            u[e] = pack(p0, p1, T());
+            tmem_st16(sc + 16 * c, u);
           }
-          tmem_st16(sc + 32 * hf + 16 * c, u);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[2 * t + hf]);
         }
         float s0, s1;
         unpair(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[2 * t + hf]);
       }
-      if (!go) break;
-      l += exchange(l);
-      if (ok) ok = mbar_wait_warp(&pv_done[t], (uint32_t)((steps - 1) & 1));
-      if (!ok) continue;                                    // the next exchange ends both warps
+      if (!ok) break;
+      if (!(ok = mbar_wait_warp(&pv_done[t], (uint32_t)((steps - 1) & 1)))) break;
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t row = (int64_t)(it.start + pos) * a.Hq + it.h * a.G + row_head;
@@ -714,12 +654,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       uint32_t some = 0;
       for (int x = 0; x < (it.tiles - cut) * 4; ++x) some |= bits[x];
 #pragma unroll 1
-      for (int c = 0; c < D / 2; c += 32) {
+      for (int c = 0; c < D; c += 32) {
         float o[32];
         tmem_ld32(oc + c, o);
         tmem_wait_ld();
         regs_after_wait(o);
-        const int col = hf * (D / 2) + c;
         if (some) {
           // infinities and NaN that the row does see, taken out of the V tiles above
           for (int x = 0; x < (it.tiles - cut) * 4; ++x)
@@ -729,7 +668,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
               const T* v = static_cast<const T*>(a.v) + (int64_t)(it.start + key) * a.v_stride + (int64_t)it.h * a.d;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const float y = col + e < a.d ? (float)v[col + e] : 0.f;
+                const float y = c + e < a.d ? (float)v[c + e] : 0.f;
                 if (!(fabsf(y) < INFINITY)) o[e] += y;
               }
             }
@@ -737,17 +676,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         if (live) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
-            if (col + e < a.d) {
+            if (c + e < a.d) {
               uint4 w;
               w.x = pack(o[e] * inv, o[e + 1] * inv, T());
               w.y = pack(o[e + 2] * inv, o[e + 3] * inv, T());
               w.z = pack(o[e + 4] * inv, o[e + 5] * inv, T());
               w.w = pack(o[e + 6] * inv, o[e + 7] * inv, T());
-              *reinterpret_cast<uint4*>(out + col + e) = w;
+              *reinterpret_cast<uint4*>(out + c + e) = w;
             }
         }
       }
-      if (live && a.lse && hf == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       tc_fence_before();
     }
     if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
@@ -756,7 +695,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 17) tmem_dealloc(tmem, 512);
+  if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
 // [tokens][heads][d] with a token stride, as boxes of 64 coordinates x `heads`
