@@ -55,7 +55,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kBadSlots = 8;               // items whose bad-key bits are kept (more than the ring can run ahead)
 constexpr int kBadTiles = 4;               // key tiles of an item that some row does not see whole: 3 at most
+constexpr int kBadWords = 4 + 4 * kBadTiles;   // what each scanning warp found in all (two words, two spare), then a bit per key
 constexpr int kBuckets = 1024;
+constexpr int kOutRow = 80;                // 32 results of a row, and 16 bytes so that rows spread over the banks
 
 template <int D>
 struct Shape {
@@ -63,8 +65,9 @@ struct Shape {
   static constexpr int tile = kTile * D * 2;           // bytes of a Q, K or V tile
   static constexpr int stages = D == 128 ? 4 : 8;
   static constexpr int off_ring = 2 * tile;
-  static constexpr int off_bad = off_ring + stages * tile;   // [kBadSlots][1 + 4 kBadTiles] words
-  static constexpr int off_bar = off_bad + kBadSlots * (1 + 4 * kBadTiles) * 4;
+  static constexpr int off_bad = off_ring + stages * tile;   // [kBadSlots][kBadWords]
+  static constexpr int off_out = off_bad + kBadSlots * kBadWords * 4;   // [8 warps][32][kOutRow] results
+  static constexpr int off_bar = off_out + 8 * 32 * kOutRow;
   static constexpr int bytes = (off_bar + 384 + 1023) / 1024 * 1024 + 1024;
 };
 
@@ -93,6 +96,12 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
       ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// the same box into L2 only
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 
 // an MN-major operand in the 128-byte swizzled layout: 128-byte rows of 64
@@ -222,6 +231,7 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const int32_t* cu, in
   __shared__ int bucket[kBuckets];
   __shared__ int warp_sum[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");   // the main grid sets itself up meanwhile
   // running maximum of the clamped bounds, then running sums of the items: 1024 at a time
   int carry = 0;
   for (int b0 = 0; b0 <= nseq; b0 += 1024) {
@@ -370,6 +380,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  if (!a.direct) asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan is written
   // the block's i-th item; every role walks the same ones
   const int all = a.direct ? 0 : *a.count * a.Hkv;
   auto item = [&](int i, Item& it) -> bool {
@@ -426,6 +437,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
                 tma_load_3d(&qmap, q_full, smem + t * S::tile + sl * kTile * 128, sl * 64, it.h * a.G,
                             it.start + it.tok[t]);
           }
+          // the next item's queries cannot be loaded before this one's last logits:
+          // have them on their way to L2 until then
+          Item nx;
+          if (ok && item(i + 1, nx))
+            for (int t = 0; t < (nx.n[1] ? 2 : 1); ++t)
+              for (int sl = 0; sl < S::slabs; ++sl) tma_prefetch_3d(&qmap, sl * 64, nx.h * a.G, nx.start + nx.tok[t]);
           for (int j = 0; ok && j < it.tiles; ++j) ok = load(&kmap, j) && load(&vmap, j);
         }
         if (!ok) atomicOr(a.status, kStatusTimeout);
@@ -505,7 +522,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       int st = 0;
       bool ok = true;
       for (int i = 0; ok && item(i, it); ++i) {
-        uint32_t* bits = bad + (i % kBadSlots) * (1 + 4 * kBadTiles);
+        uint32_t* bits = bad + (i % kBadSlots) * kBadWords;
+        uint32_t found = 0;
         const int cut = first_cut(it);
         for (int j = 0; j < it.tiles; ++j) {
           for (int kv = 0; kv < 2; ++kv, ++st) {
@@ -517,8 +535,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
               for (int gr = 0; gr < 2; ++gr) {
                 const int key = w * 64 + gr * 32 + lane;
                 bool any = false;
+                // keys up to the item's first token are seen by all its rows
+                const int chunks = j * kTile + w * 64 + gr * 32 + 31 <= it.tok[0] ? 0 : D / 8;
 #pragma unroll 4
-                for (int u = 0; u < D / 8; ++u) {
+                for (int u = 0; u < chunks; ++u) {
                   uint4* p = reinterpret_cast<uint4*>(vt + (u >> 3) * kTile * 128 + key * 128 + (((u & 7) ^ (key & 7)) << 4));
                   uint4 x = *p;
                   const uint32_t b0 = bad_halves<T>(x.x), b1 = bad_halves<T>(x.y), b2 = bad_halves<T>(x.z), b3 = bad_halves<T>(x.w);
@@ -531,8 +551,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
                   }
                 }
                 const uint32_t m = __ballot_sync(kFull, any);
-                if (lane == 0) bits[1 + (j - cut) * 4 + w * 2 + gr] = m;
+                found |= m;
+                if (lane == 0) bits[4 + (j - cut) * 4 + w * 2 + gr] = m;
               }
+              if (lane == 0) bits[w] = found;
               fence_async_smem();
               __syncwarp();
             }
@@ -555,6 +577,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
     const uint32_t sc = tmem + lanes + kColS + t * 128, oc = tmem + lanes + kColO + t * 128;
     const int row_tok = r / a.G, row_head = r % a.G;
     const float cl = a.scale_log2;
+    uint8_t* stage = smem + S::off_out + warp * 32 * kOutRow;
+    // the rows that this lane writes results of: token in the tile, elements from the tile's first
+    int out_tok[4], out_off[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int y = (warp & 3) * 32 + k * 8 + (lane >> 2);
+      out_tok[k] = y / a.G;
+      out_off[k] = (out_tok[k] * a.Hq + y % a.G) * a.d;
+    }
     int steps = 0;
     bool ok = true;
     for (int i = 0; ok && item(i, it); ++i) {
@@ -648,16 +679,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t row = (int64_t)(it.start + pos) * a.Hq + it.h * a.G + row_head;
-      T* out = static_cast<T*>(a.out) + row * a.d;
-      const uint32_t* bits = bad + (i % kBadSlots) * (1 + 4 * kBadTiles) + 1;
+      T* out = static_cast<T*>(a.out) + ((int64_t)(it.start + it.tok[t]) * a.Hq + it.h * a.G) * a.d;   // the tile's first
       const int cut = first_cut(it);
-      uint32_t some = 0;
-      for (int x = 0; x < (it.tiles - cut) * 4; ++x) some |= bits[x];
-#pragma unroll 1
+      const uint32_t* bits = bad + (i % kBadSlots) * kBadWords;
+      const uint32_t some = it.tiles > cut ? bits[0] | bits[1] : 0u;
+      bits += 4;
+      float all_o[D / 32][32];
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) tmem_ld32(oc + 32 * c, all_o[c]);
+      tmem_wait_ld();
+#pragma unroll
       for (int c = 0; c < D; c += 32) {
-        float o[32];
-        tmem_ld32(oc + c, o);
-        tmem_wait_ld();
+        float(&o)[32] = all_o[c / 32];
         regs_after_wait(o);
         if (some) {
           // infinities and NaN that the row does see, taken out of the V tiles above
@@ -673,18 +706,25 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
               }
             }
         }
-        if (live) {
+        // through shared memory, so that four neighbouring lanes write 64 bytes
+        // of a row (a lane writing its own row touches a line per lane)
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            if (c + e < a.d) {
-              uint4 w;
-              w.x = pack(o[e] * inv, o[e + 1] * inv, T());
-              w.y = pack(o[e + 2] * inv, o[e + 3] * inv, T());
-              w.z = pack(o[e + 4] * inv, o[e + 5] * inv, T());
-              w.w = pack(o[e + 6] * inv, o[e + 7] * inv, T());
-              *reinterpret_cast<uint4*>(out + c + e) = w;
-            }
+        for (int e = 0; e < 32; e += 8) {
+          uint4 w;
+          w.x = pack(o[e] * inv, o[e + 1] * inv, T());
+          w.y = pack(o[e + 2] * inv, o[e + 3] * inv, T());
+          w.z = pack(o[e + 4] * inv, o[e + 5] * inv, T());
+          w.w = pack(o[e + 6] * inv, o[e + 7] * inv, T());
+          *reinterpret_cast<uint4*>(stage + lane * kOutRow + e * 2) = w;
         }
+        __syncwarp();
+        const int col = c + (lane & 3) * 8;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (out_tok[k] < a.tq && it.tok[t] + out_tok[k] < it.len && col < a.d)
+            *reinterpret_cast<uint4*>(out + out_off[k] + col) =
+                *reinterpret_cast<const uint4*>(stage + (k * 8 + (lane >> 2)) * kOutRow + (lane & 3) * 16);
+        __syncwarp();
       }
       if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       tc_fence_before();
@@ -720,8 +760,17 @@ int launch_main(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap&
                 cudaStream_t st) {
   const int e = ensure_dyn_smem(reinterpret_cast<const void*>(prompt_kernel<D, T>), Shape<D>::bytes);
   if (e) return e;
-  prompt_kernel<D, T><<<grid, kThreads, Shape<D>::bytes, st>>>(qm, km, vm, a);
-  return (int)cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<D>::bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = a.direct ? 0 : 1;   // beside the plan's kernel
+  return (int)cudaLaunchKernelEx(&cfg, prompt_kernel<D, T>, qm, km, vm, a);
 }
 
 }  // namespace
@@ -787,6 +836,7 @@ extern "C" int tq_attn_prompt(tq_handle h, const void* q, const void* k, const v
   if (dtype != TQ_BF16 && dtype != TQ_F16) return set_error(TQ_EUNSUPPORTED, "%s: dtype %d (need TQ_BF16 or TQ_F16)", fn, dtype);
   if (nseq < 0 || total < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0)
     return set_error(TQ_EINVAL, "%s: bad shape (nseq=%d total=%lld Hq=%d Hkv=%d)", fn, nseq, (long long)total, Hq, Hkv);
+  if (Hq > INT32_MAX / (128 * h->d)) return set_error(TQ_EUNSUPPORTED, "%s: Hq = %d", fn, Hq);
   if (Hq / Hkv > 128) return set_error(TQ_EUNSUPPORTED, "%s: %d query heads per kv-head (at most 128)", fn, Hq / Hkv);
   if (nseq > TQ_MAX_SEQS) return set_error(TQ_EUNSUPPORTED, "%s: nseq = %d (at most %d)", fn, nseq, TQ_MAX_SEQS);
   if (total > INT32_MAX / 128 || (total + nseq) * Hkv > INT32_MAX / 2)
