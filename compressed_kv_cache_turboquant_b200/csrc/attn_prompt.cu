@@ -57,7 +57,7 @@ constexpr int kBadSlots = 8;               // items whose bad-key bits are kept 
 constexpr int kBadTiles = 4;               // key tiles of an item that some row does not see whole: 3 at most
 constexpr int kBadWords = 4 + 4 * kBadTiles;   // what each scanning warp found in all (two words, two spare), then a bit per key
 constexpr int kBuckets = 1024;
-constexpr int kOutRow = 80;                // 32 results of a row, and 16 bytes so that rows spread over the banks
+constexpr int kBarBytes = 320;             // room for the barriers and the tensor-memory address
 
 template <int D>
 struct Shape {
@@ -65,10 +65,10 @@ struct Shape {
   static constexpr int tile = kTile * D * 2;           // bytes of a Q, K or V tile
   static constexpr int stages = D == 128 ? 4 : 8;
   static constexpr int off_ring = 2 * tile;
-  static constexpr int off_bad = off_ring + stages * tile;   // [kBadSlots][kBadWords]
-  static constexpr int off_out = off_bad + kBadSlots * kBadWords * 4;   // [8 warps][32][kOutRow] results
-  static constexpr int off_bar = off_out + 8 * 32 * kOutRow;
-  static constexpr int bytes = (off_bar + 384 + 1023) / 1024 * 1024 + 1024;
+  static constexpr int off_out = off_ring + stages * tile;   // [8 warps][32 rows][128 bytes] results
+  static constexpr int off_bad = off_out + 8 * 32 * 128;     // [kBadSlots][kBadWords]
+  static constexpr int off_bar = off_bad + kBadSlots * kBadWords * 4;
+  static constexpr int bytes = off_bar + kBarBytes + 16 + 1024;
 };
 
 struct PromptArgs {
@@ -81,6 +81,7 @@ struct PromptArgs {
   int64_t v_stride;
   int total, nseq, Hq, Hkv, d, G, tq;   // tq = 128 / G tokens of a row tile
   int direct;             // no plan: block i finds item i / Hkv
+  int out_box;            // tokens in 32 rows, where they are whole (0: they are not)
   float scale_log2;
   int* status;
 };
@@ -96,6 +97,12 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
       ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 
 // the same box into L2 only
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const int32_t* cu, in
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-              const __grid_constant__ CUtensorMap vmap, PromptArgs a) {
+              const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap, PromptArgs a) {
   using S = Shape<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -322,7 +329,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   uint64_t* pv_done = p_ready + 4;       // [2] MMA commit: value product done
   uint64_t* done = pv_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  int4* direct_item = reinterpret_cast<int4*>(smem + S::off_bar + 320);
+  int4* direct_item = reinterpret_cast<int4*>(smem + S::off_bar + kBarBytes);
+  static_assert((3 * S::stages + 11) * 8 + 4 <= kBarBytes && S::bytes <= 232448, "shared memory");
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -382,21 +390,24 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
 
   if (!a.direct) asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan is written
   // the block's i-th item; every role walks the same ones
-  const int all = a.direct ? 0 : *a.count * a.Hkv;
+  const int all = a.direct ? 0 : __ldcg(a.count) * a.Hkv;
+  // (`ahead` holds the entry of item i, read an item earlier; ld.cg, since the
+  // plan may still be writing when this grid starts)
+  auto entry = [&](int i) -> int4 {
+    if (a.direct) return i == 0 ? *direct_item : make_int4(0, 0, -1, 0);
+    // there and back over the sorted list, so that the blocks' sums stay close
+    const int x = i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (x >= all) return make_int4(0, 0, -1, 0);
+    int4 e = __ldcg(a.items + x / a.Hkv);
+    e.w = x % a.Hkv;
+    return e;
+  };
+  int4 ahead = entry(0);
   auto item = [&](int i, Item& it) -> bool {
-    int4 e;
-    if (a.direct) {
-      if (i > 0) return false;
-      e = *direct_item;
-      if (e.z < 0) return false;
-      it.h = blockIdx.x % a.Hkv;
-    } else {
-      // there and back over the sorted list, so that the blocks' sums stay close
-      const int x = i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      if (x >= all) return false;
-      e = __ldg(a.items + x / a.Hkv);
-      it.h = x % a.Hkv;
-    }
+    const int4 e = ahead;
+    if (e.z < 0) return false;
+    ahead = entry(i + 1);
+    it.h = a.direct ? blockIdx.x % a.Hkv : e.w;
     it.start = e.x;
     it.len = e.y;
 #pragma unroll
@@ -439,10 +450,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
           }
           // the next item's queries cannot be loaded before this one's last logits:
           // have them on their way to L2 until then
-          Item nx;
-          if (ok && item(i + 1, nx))
-            for (int t = 0; t < (nx.n[1] ? 2 : 1); ++t)
-              for (int sl = 0; sl < S::slabs; ++sl) tma_prefetch_3d(&qmap, sl * 64, nx.h * a.G, nx.start + nx.tok[t]);
+          if (ok && ahead.z >= 0)
+            for (int t = 0; t < 2; ++t)
+              for (int sl = 0; sl < S::slabs; ++sl)
+                tma_prefetch_3d(&qmap, sl * 64, ahead.w * a.G, min(ahead.x + (ahead.z * 2 + t) * a.tq, a.total - 1));
           for (int j = 0; ok && j < it.tiles; ++j) ok = load(&kmap, j) && load(&vmap, j);
         }
         if (!ok) atomicOr(a.status, kStatusTimeout);
@@ -576,16 +587,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t sc = tmem + lanes + kColS + t * 128, oc = tmem + lanes + kColO + t * 128;
     const int row_tok = r / a.G, row_head = r % a.G;
+    const int warp_tok = __shfl_sync(kFull, row_tok, 0);    // of the warp's first row
     const float cl = a.scale_log2;
-    uint8_t* stage = smem + S::off_out + warp * 32 * kOutRow;
-    // the rows that this lane writes results of: token in the tile, elements from the tile's first
-    int out_tok[4], out_off[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int y = (warp & 3) * 32 + k * 8 + (lane >> 2);
-      out_tok[k] = y / a.G;
-      out_off[k] = (out_tok[k] * a.Hq + y % a.G) * a.d;
-    }
+    uint8_t* stage = smem + S::off_out + warp * 32 * 128;
     int steps = 0;
     bool ok = true;
     for (int i = 0; ok && item(i, it); ++i) {
@@ -603,12 +607,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) regs_after_wait(x[c]);
-        const int lim = pos - j * kTile;                    // keys past it take no part
-        if (__any_sync(kFull, lim < kTile - 1)) {
+        // keys past the row's own take no part; a group of 32 that the warp's
+        // first row sees whole needs no look
+        const int lim = pos - j * kTile, low = it.tok[t] + warp_tok - j * kTile;
+        if (low < kTile - 1) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
+            if (low < 32 * c + 31) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[c][e] = 32 * c + e <= lim ? x[c][e] : -INFINITY;
+              for (int e = 0; e < 32; ++e) x[c][e] = 32 * c + e <= lim ? x[c][e] : -INFINITY;
+            }
         }
         float mx[4];
 #pragma unroll
@@ -679,57 +687,76 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t row = (int64_t)(it.start + pos) * a.Hq + it.h * a.G + row_head;
-      T* out = static_cast<T*>(a.out) + ((int64_t)(it.start + it.tok[t]) * a.Hq + it.h * a.G) * a.d;   // the tile's first
       const int cut = first_cut(it);
       const uint32_t* bits = bad + (i % kBadSlots) * kBadWords;
       const uint32_t some = it.tiles > cut ? bits[0] | bits[1] : 0u;
       bits += 4;
-      float all_o[D / 32][32];
+      // whole tokens of the group in the warp's rows, all of the sequence: one TMA
+      // store per 64 coordinates, which nothing waits for but the next use of the
+      // buffer (stores by the lanes hold the warps for as long as memory takes)
+      const int first = it.tok[t] + warp_tok, tokens = a.out_box;
+      const bool whole = tokens > 0 && first + tokens <= it.len;
+#pragma unroll 1
+      for (int sl = 0; sl < S::slabs; ++sl) {
+        float o[2][32];
+        tmem_ld32(oc + 64 * sl, o[0]);
+        tmem_ld32(oc + 64 * sl + 32, o[1]);
+        tmem_wait_ld();
+        if (lane == 0) bulk_wait_read<0>();                 // the buffer's last store has read it
+        __syncwarp();
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) tmem_ld32(oc + 32 * c, all_o[c]);
-      tmem_wait_ld();
+        for (int c = 0; c < 2; ++c) {
+          regs_after_wait(o[c]);
+          if (some) {
+            // infinities and NaN that the row does see, taken out of the V tiles above
+            for (int x = 0; x < (it.tiles - cut) * 4; ++x)
+              for (uint32_t b = bits[x]; b; b &= b - 1) {
+                const int key = cut * kTile + x * 32 + __ffs(b) - 1;
+                if (!live || key > pos) continue;
+                const T* v = static_cast<const T*>(a.v) + (int64_t)(it.start + key) * a.v_stride + (int64_t)it.h * a.d;
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        float(&o)[32] = all_o[c / 32];
-        regs_after_wait(o);
-        if (some) {
-          // infinities and NaN that the row does see, taken out of the V tiles above
-          for (int x = 0; x < (it.tiles - cut) * 4; ++x)
-            for (uint32_t b = bits[x]; b; b &= b - 1) {
-              const int key = cut * kTile + x * 32 + __ffs(b) - 1;
-              if (!live || key > pos) continue;
-              const T* v = static_cast<const T*>(a.v) + (int64_t)(it.start + key) * a.v_stride + (int64_t)it.h * a.d;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float y = c + e < a.d ? (float)v[c + e] : 0.f;
-                if (!(fabsf(y) < INFINITY)) o[e] += y;
+                for (int e = 0; e < 32; ++e) {
+                  const float y = 64 * sl + 32 * c + e < a.d ? (float)v[64 * sl + 32 * c + e] : 0.f;
+                  if (!(fabsf(y) < INFINITY)) o[c][e] += y;
+                }
               }
-            }
-        }
-        // through shared memory, so that four neighbouring lanes write 64 bytes
-        // of a row (a lane writing its own row touches a line per lane)
+          }
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint4 w;
-          w.x = pack(o[e] * inv, o[e + 1] * inv, T());
-          w.y = pack(o[e + 2] * inv, o[e + 3] * inv, T());
-          w.z = pack(o[e + 4] * inv, o[e + 5] * inv, T());
-          w.w = pack(o[e + 6] * inv, o[e + 7] * inv, T());
-          *reinterpret_cast<uint4*>(stage + lane * kOutRow + e * 2) = w;
+          for (int u = 0; u < 4; ++u) {
+            const float* y = o[c] + 8 * u;
+            uint4 w;
+            w.x = pack(y[0] * inv, y[1] * inv, T());
+            w.y = pack(y[2] * inv, y[3] * inv, T());
+            w.z = pack(y[4] * inv, y[5] * inv, T());
+            w.w = pack(y[6] * inv, y[7] * inv, T());
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + u) ^ (lane & 7)) << 4)) = w;
+          }
         }
-        __syncwarp();
-        const int col = c + (lane & 3) * 8;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (out_tok[k] < a.tq && it.tok[t] + out_tok[k] < it.len && col < a.d)
-            *reinterpret_cast<uint4*>(out + out_off[k] + col) =
-                *reinterpret_cast<const uint4*>(stage + (k * 8 + (lane >> 2)) * kOutRow + (lane & 3) * 16);
-        __syncwarp();
+        if (whole) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&omap, stage, sl * 64, it.h * a.G, it.start + first);
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+#pragma unroll 1
+          for (int k = 0; k < 32; k += 4) {                 // eight lanes a row
+            const int x = k + (lane >> 3), y = (warp & 3) * 32 + x, tok = y / a.G, col = sl * 64 + (lane & 7) * 8;
+            if (tok < a.tq && it.tok[t] + tok < it.len && col < a.d)
+              *reinterpret_cast<uint4*>(static_cast<T*>(a.out) +
+                                        ((int64_t)(it.start + it.tok[t] + tok) * a.Hq + it.h * a.G + y % a.G) * a.d + col) =
+                  *reinterpret_cast<const uint4*>(stage + x * 128 + (((lane & 7) ^ (x & 7)) << 4));
+          }
+          __syncwarp();
+        }
       }
       if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       tc_fence_before();
     }
     if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
+    if (lane == 0) bulk_wait_all();                         // the buffer is read until then
   }
   __syncwarp();
   tc_fence_before();
@@ -756,7 +783,7 @@ bool token_map(CUtensorMap* m, const void* base, bool bf, int d, int H, int64_t 
 int64_t most_items(int nseq, int64_t total, int tq) { return total / (2 * tq) + nseq; }
 
 template <int D, typename T>
-int launch_main(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const PromptArgs& a, int grid,
+int launch_main(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& om, const PromptArgs& a, int grid,
                 cudaStream_t st) {
   const int e = ensure_dyn_smem(reinterpret_cast<const void*>(prompt_kernel<D, T>), Shape<D>::bytes);
   if (e) return e;
@@ -770,7 +797,7 @@ int launch_main(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap&
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early;
   cfg.numAttrs = a.direct ? 0 : 1;   // beside the plan's kernel
-  return (int)cudaLaunchKernelEx(&cfg, prompt_kernel<D, T>, qm, km, vm, a);
+  return (int)cudaLaunchKernelEx(&cfg, prompt_kernel<D, T>, qm, km, vm, om, a);
 }
 
 }  // namespace
@@ -794,10 +821,12 @@ int launch_prompt(const tq_ctx* h, const void* q, const void* k, const void* v, 
   // never 0: masked logits are -infinity before they are scaled, and 0 times that is NaN
   a.scale_log2 = std::max(scale * 1.4426950408889634f, 1e-37f);
   a.status = h->dev.status;
-  CUtensorMap qm, km, vm;
+  a.out_box = 32 % a.G ? 0 : 32 / a.G;
+  CUtensorMap qm, km, vm, om;
   if (!token_map(&qm, q, bf, h->d, Hq, total, total > 1 ? q_stride : (int64_t)Hq * h->d, a.G, a.tq) ||
       !token_map(&km, k, bf, h->d, Hkv, total, total > 1 ? k_stride : (int64_t)Hkv * h->d, 1, kTile) ||
-      !token_map(&vm, v, bf, h->d, Hkv, total, vs, 1, kTile))
+      !token_map(&vm, v, bf, h->d, Hkv, total, vs, 1, kTile) ||
+      !token_map(&om, out, bf, h->d, Hq, total, (int64_t)Hq * h->d, a.G, std::max(a.out_box, 1)))
     return (int)cudaErrorInvalidValue;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t work = most_items(nseq, total, a.tq) * Hkv;
@@ -812,8 +841,8 @@ int launch_prompt(const tq_ctx* h, const void* q, const void* k, const void* v, 
   }
   const int grid = (int)std::min<int64_t>(work, h->sm_count);
   if (h->d <= 64)
-    return bf ? launch_main<64, __nv_bfloat16>(qm, km, vm, a, grid, st) : launch_main<64, __half>(qm, km, vm, a, grid, st);
-  return bf ? launch_main<128, __nv_bfloat16>(qm, km, vm, a, grid, st) : launch_main<128, __half>(qm, km, vm, a, grid, st);
+    return bf ? launch_main<64, __nv_bfloat16>(qm, km, vm, om, a, grid, st) : launch_main<64, __half>(qm, km, vm, om, a, grid, st);
+  return bf ? launch_main<128, __nv_bfloat16>(qm, km, vm, om, a, grid, st) : launch_main<128, __half>(qm, km, vm, om, a, grid, st);
 }
 
 }  // namespace tqi
