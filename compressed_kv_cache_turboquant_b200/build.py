@@ -27,7 +27,7 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xc
 
 # Kernels that move registers between their warpgroups (setmaxnreg): the
 # assembler only does that in a unit compiled as a whole program.
-WHOLE_PROGRAM = {"attn_tree.cu", "attn_prompt.cu"}
+WHOLE_PROGRAM = {"attn_tree.cu", "attn_tree_tc.cu", "attn_prompt.cu"}
 
 
 def sources():

@@ -38,21 +38,18 @@
 #include <cmath>
 #include <type_traits>
 
-#include "sm100_common.cuh"
+#include "attn_common.cuh"
 #include "tq_internal.h"
 
 namespace tqi {
 namespace {
 
-using namespace sm100;
+using namespace attn;
 
 constexpr int kTile = 128;                 // rows of a row tile, keys of a key tile
 constexpr int kThreads = 384;
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;   // 2 x 208 + 88 = 3 x 168, the registers at launch
 constexpr uint32_t kColS = 0, kColO = 256; // S/P of tiles 0, 1 at 0, 128; O at 256, 384
-constexpr float kLazy = 8.f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kBadSlots = 8;               // items whose bad-key bits are kept (more than the ring can run ahead)
 constexpr int kBadTiles = 4;               // key tiles of an item that some row does not see whole: 3 at most
 constexpr int kBadWords = 4 + 4 * kBadTiles;   // what each scanning warp found in all (two words, two spare), then a bit per key
@@ -86,93 +83,6 @@ struct PromptArgs {
   int* status;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
-      ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
-               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-
-// the same box into L2 only
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-
-// an MN-major operand in the 128-byte swizzled layout: 128-byte rows of 64
-// elements along N, 8-row atoms 1024 bytes apart along K, the next 64 elements
-// of N lbo bytes further
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t lbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
-}
-
-// The issuing warp runs its loop as a whole, so that descriptors and addresses
-// stay in uniform registers (a loop of one thread moves each operand there one
-// by one: 130 cycles a product instead of the 64 it takes); `lead` is set in
-// the lane whose instructions count.
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t lead;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(lead));
-  return lead;
-}
-
-// D (+)= A B^T, both from shared memory
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
-}
-
-// A from tensor memory
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
-}
-
-__device__ __forceinline__ void commit(uint64_t* bar, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
-      ::"r"(smem_u32(bar)), "r"(lead)
-      : "memory");
-}
-
-// keeps every use of registers that tcgen05.ld fills behind its wait
-__device__ __forceinline__ void regs_after_wait(float (&r)[32]) {
-  asm volatile(""
-               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])::"memory");
-}
-
-// the largest, or NaN where one of them is
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 // two float32 in one 64-bit register: sm_100 multiplies and adds them as a pair
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t d;
@@ -191,15 +101,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
-}
-
-__device__ __forceinline__ uint32_t pack(float lo, float hi, __nv_bfloat16) {
-  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t pack(float lo, float hi, __half) {
-  const __half2 r = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 template <typename T>
@@ -763,20 +664,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
-}
-
-// [tokens][heads][d] with a token stride, as boxes of 64 coordinates x `heads`
-// heads x `tokens` tokens in 128-byte swizzled rows
-bool token_map(CUtensorMap* m, const void* base, bool bf, int d, int H, int64_t total, int64_t stride, int heads, int tokens) {
-  const EncodeTiledFn enc = encode_tiled_fn();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)total};
-  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
-  cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims,
-             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // more items than this never come out of `total` tokens in `nseq` sequences

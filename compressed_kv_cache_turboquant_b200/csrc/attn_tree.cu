@@ -38,13 +38,13 @@
 #include <cmath>
 #include <type_traits>
 
-#include "sm100_common.cuh"
-#include "tq_internal.h"
+#include "attn_tree.cuh"
 
 namespace tqi {
 namespace {
 
-using namespace sm100;
+using namespace attn;
+using namespace tree;
 
 constexpr int kKeys = 64;            // keys of a tile
 constexpr int kWarps = 4;            // consumer warps, 16 keys of a tile each
@@ -53,9 +53,6 @@ constexpr int kBlocksPerSm = 2;
 // registers: 128 a thread at launch; the consumers take what the other
 // warpgroup gives back (216 + 40 = 2 x 128)
 constexpr int kRegsConsumer = 216, kRegsProducer = 40;
-constexpr float kLazy = 8.f;         // the running maximum moves when a logit passes it by 2^8
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 // what the shared window holds, by padded dimension and rows of a block
 template <int D, int MT>
@@ -76,25 +73,6 @@ struct Shape {
   static constexpr int off_bar = off_ml + 2 * kWarps * rows * 4;
   static constexpr int bytes = off_bar + 512 + 1024;
 };
-
-// the part of a workspace that a block owns: two records [rows][D + 2] (value
-// sum, maximum, sum) and the item that its first record belongs to
-struct Cut {
-  int64_t begin, end;  // the item's units
-  int b, h, rb, partial;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
@@ -145,68 +123,6 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t a, uint32_t b, int j) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// the remainders of that rounding, as bf16 again
-__device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t rounded) {
-  return pack_bf16(lo - __uint_as_float(rounded << 16), hi - __uint_as_float(rounded & 0xFFFF0000u));
-}
-
-struct Seq {
-  int ctx, T, drafts, tiles, blocks;  // blocks of rows
-};
-
-__device__ __forceinline__ Seq seq_of(const TreeArgs& a, int b, int rows_per_block) {
-  Seq s;
-  const int cap = a.max_pages * a.page;
-  s.drafts = a.draft_lens ? min(max(__ldg(a.draft_lens + b), 0), a.n) : a.n;
-  s.ctx = max(__ldg(a.ctx_lens + b), 0);
-  s.T = (int)min((int64_t)s.ctx + s.drafts, (int64_t)cap);
-  s.tiles = (s.T + kKeys - 1) / kKeys;
-  s.blocks = (s.drafts * (a.Hq / a.Hkv) + rows_per_block - 1) / rows_per_block;
-  return s;
-}
-
-__device__ __forceinline__ int64_t units_of(const TreeArgs& a, const Seq& s) {
-  return (int64_t)a.Hkv * s.blocks * s.tiles;
-}
-
-// one work item's share of a block: tiles lo .. hi - 1 of kv-head h, rows block rb
-struct Piece {
-  Seq s;
-  int b, h, rb, lo, hi;
-  int64_t begin;  // first unit of the item
-};
-
-// walks the pieces of units u .. end - 1; b, base: a sequence at or before u's and its first unit
-struct Walk {
-  int64_t u, end, base;
-  int b;
-  __device__ __forceinline__ bool next(const TreeArgs& a, int rows_per_block, Piece& p) {
-    if (u >= end) return false;
-    p.s = seq_of(a, b, rows_per_block);
-    int64_t n = units_of(a, p.s);
-    while (u - base >= n) {
-      base += n;
-      ++b;
-      p.s = seq_of(a, b, rows_per_block);
-      n = units_of(a, p.s);
-    }
-    const int64_t item = (u - base) / p.s.tiles;
-    p.b = b;
-    p.h = (int)(item / p.s.blocks);
-    p.rb = (int)(item % p.s.blocks);
-    p.begin = base + item * p.s.tiles;
-    p.lo = (int)(u - p.begin);
-    p.hi = (int)min((int64_t)p.s.tiles, p.lo + (end - u));
-    u += p.hi - p.lo;
-    return true;
-  }
-};
-
 template <typename T>
 __device__ __forceinline__ void store_pair(T* p, float x, float y);
 template <>
@@ -240,8 +156,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::off_bar);
   uint64_t* empty = full + S::stages;
   uint64_t* valid = empty + S::stages;                    // per stage: bit k = key k is there
-  int64_t* found = reinterpret_cast<int64_t*>(valid + S::stages);   // first sequence, its first unit
-  int64_t* part = found + 2;                              // [2 kWarps]
+  int64_t* found = reinterpret_cast<int64_t*>(valid + S::stages);   // scratch of range_of_block
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -251,47 +166,11 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     }
     fence_mbar_init();
   }
-  // units of all sequences, then the sequence that this block's range begins in
-  int64_t sum = 0;
-  for (int b = threadIdx.x; b < a.B; b += kThreads) {
-    const Seq s = seq_of(a, b, S::rows);
-    sum += units_of(a, s);
-    const int cl = __ldg(a.ctx_lens + b);
-    if (blockIdx.x == 0 && (cl < 0 || (int64_t)s.ctx + s.drafts > s.T || (a.draft_lens && __ldg(a.draft_lens + b) != s.drafts)))
-      atomicOr(a.status, kStatusRange);
-  }
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  if (lane == 0) part[warp] = sum;
-  __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < 2 * kWarps; ++w) total += part[w];
-  // no more blocks than units, so that none between two others is idle
-  const int64_t blocks = min((int64_t)gridDim.x, total);
-  const bool idle = blockIdx.x >= blocks;
-  const int64_t u0 = idle ? 0 : total * blockIdx.x / blocks, u1 = idle ? 0 : total * (blockIdx.x + 1) / blocks;
-  if (warp == 0 && !idle) {
-    int64_t base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int64_t mine = b0 + lane < a.B ? units_of(a, seq_of(a, b0 + lane, S::rows)) : 0;
-      int64_t upto = mine;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(kFull, upto, o);
-        if (lane >= o) upto += x;
-      }
-      const uint32_t past = __ballot_sync(kFull, base + upto > u0);
-      if (past) {
-        if (lane == __ffs(past) - 1) found[0] = b0 + lane, found[1] = base + upto - mine;
-        break;
-      }
-      base += __shfl_sync(kFull, upto, 31);
-    }
-  }
-  __syncthreads();
-  if (idle) {
+  Walk<kKeys> walk;
+  if (!range_of_block<kKeys, kThreads>(a, S::rows, found, walk)) {
     if (threadIdx.x == 0 && cuts) cuts[blockIdx.x].partial = 0;
     return;
   }
-  Walk walk{u0, u1, found[1], (int)found[0]};
   Piece p;
 
   if (warp >= kWarps) {
@@ -713,16 +592,14 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, int grid, c
   __shared__ int64_t total_sm;
   __shared__ int64_t part[4];
   int64_t sum = 0;
-  for (int b = threadIdx.x; b < a.B; b += 128) sum += units_of(a, seq_of(a, b, S::rows));
+  for (int b = threadIdx.x; b < a.B; b += 128) sum += units_of(a, seq_of<kKeys>(a, b, S::rows));
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
   __syncthreads();
   if (threadIdx.x == 0) total_sm = part[0] + part[1] + part[2] + part[3];
   __syncthreads();
-  const int64_t total = total_sm, blocks = min((int64_t)grid, total);
-  if (total * (i - 1) / blocks > cut.begin) return;          // an earlier cut is this item's first
-  int last = i;
-  while (last + 1 < blocks && total * (last + 1) / blocks < cut.end) ++last;
+  int last;
+  if (!first_cut_of(cut, i, grid, total_sm, last)) return;
   const int G = a.Hq / a.Hkv;
   const int drafts = a.draft_lens ? min(max(__ldg(a.draft_lens + cut.b), 0), a.n) : a.n;
   const int rows = min(S::rows, drafts * G - cut.rb * S::rows);
@@ -802,12 +679,14 @@ int tree_grid(const tq_ctx* h, int B, int Hkv, int64_t row_blocks, int64_t tiles
 
 size_t tree_workspace(const tq_ctx* h, int B, int n, int Hq, int Hkv) {
   if (B == 0 || n == 0 || Hq == 0) return 0;
+  if (tree_tc_supported(h, n, Hq, Hkv)) return tree_tc_workspace(h, n, Hq, Hkv);
   const int64_t rows = (int64_t)n * (Hq / Hkv);
   const int mt = row_tiles(h->d, rows), grid = h->sm_count * kBlocksPerSm;
   return ((size_t)grid * sizeof(Cut) + 255) / 256 * 256 + (size_t)grid * 2 * 16 * mt * (padded(h->d) + 2) * 4;
 }
 
 int launch_tree(const tq_ctx* h, const TreeArgs& a, int dtype, void* workspace, void* stream) {
+  if (tree_tc_supported(h, a.n, a.Hq, a.Hkv)) return launch_tree_tc(h, a, dtype, workspace, stream);
   int box = kKeys;
   while (a.page % box) box /= 2;  // page pieces that a tile never splits: 8, 16, 32 or 64 keys
   CUtensorMap km, vm;

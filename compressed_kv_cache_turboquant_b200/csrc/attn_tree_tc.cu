@@ -1,0 +1,692 @@
+// Attention of many drafted tokens per sequence over the 8-bit paged cache, on
+// the tensor cores' own path (tcgen05, sm_100a).
+//
+// The arithmetic is that of attn_tree.cu: both products run on the integer
+// codes, exact in 16 bits, with the scales on the float32 logits and on the
+// weights (rounded once to bf16; for fp16 results the remainder of that rounding
+// takes a second product).  A row is a (token, head of a kv-head's group) pair,
+// 128 / G tokens of a group of G heads in a tile of 128 rows, one or two tiles a
+// block; queries enter as they are.  Against attn_tree.cu's blocks of 32 rows
+// the codes of a key tile are converted once for up to 256 rows.
+//
+// Warps (640 threads, one block per SM, persistent over equal ranges of 128-key
+// tiles; what a cut divides is joined by tree_tc_merge_kernel):
+//   0-3, 4-7  softmax of row tile 0, 1: thread = row (TMEM lane), a tile's logits
+//             read twice from tensor memory (maximum; weights, written over them)
+//   8         TMA of the item's queries and of raw code tiles, a page piece at a
+//             time, K and V alternating in a ring
+//   9         the MMA issuer
+//   12-19     converters: raw codes -> swizzled 16-bit operand tiles (one K tile,
+//             two V tiles), scales and the bits of the keys that are there
+// Tensor memory: S/P of tiles 0, 1 at 0, 128; O at 256, 384.  The weights of the
+// first 64 keys take 32 columns from the start of their tile's S, those of the
+// other 64 from its middle, and remainders follow each.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "attn_tree.cuh"
+
+namespace tqi {
+namespace {
+
+using namespace attn;
+using namespace tree;
+
+constexpr int kTile = 128;                    // rows of a row tile, keys of a tile
+constexpr int kThreads = 640;
+constexpr int kConverters = 8;
+constexpr int kRegsSoftmax = 128, kRegsOther = 72;   // 2 x 128 + 3 x 72 <= 5 x 96, the registers at launch
+constexpr uint32_t kColS = 0, kColO = 256;
+constexpr int kBarBytes = 640;   // barriers, valid bits, scratch, the tensor-memory address
+
+template <int D, int NT>
+struct Shape {
+  static constexpr int slabs = D / 64;
+  static constexpr int tile = kTile * D * 2;  // bytes of a 16-bit operand tile
+  static constexpr int raw = kTile * D;       // bytes of a raw tile
+  static constexpr int scales = 2 * kTile * 4;   // K's and V's, with a K tile
+  static constexpr int stages = D == 128 ? (NT == 2 ? 3 : 5) : 8;
+  static constexpr int off_k = NT * tile;
+  static constexpr int off_v = off_k + tile;
+  static constexpr int off_raw = off_v + 2 * tile;
+  static constexpr int off_rs = off_raw + stages * raw;          // [stages][scales]
+  static constexpr int off_sc = off_rs + stages * scales;        // [2 tiles in turn][K scales x logit scale, V scales][128]
+  static constexpr int off_valid = off_sc + 2 * scales;          // [2][4] words
+  static constexpr int off_bar = off_valid + 2 * 16;
+  static constexpr int bytes = off_bar + kBarBytes + 1024;
+  static constexpr int rows = NT * kTile;
+};
+
+// four int8 codes -> two 16-bit pairs.  bf16: the low seven bits under 0x43 are
+// 128 + them, the sign bit alone 128 or 256; fp16: a byte + 128 under 0x64 is
+// 1024 + 128 + the code
+__device__ __forceinline__ uint2 codes4(uint32_t w, __nv_bfloat16) {
+  uint2 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t t = prmt(w, 0x43434343u, i ? 0x4342u : 0x4140u);
+    const uint32_t m = t & 0xFF7FFF7Fu, s = t & 0xFF80FF80u;
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&s));
+    (i ? r.y : r.x) = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return r;
+}
+__device__ __forceinline__ uint2 codes4(uint32_t w, __half) {
+  const uint32_t x = w ^ 0x80808080u;
+  const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));
+  uint2 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t t = prmt(x, 0x64646464u, i ? 0x4342u : 0x4140u);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&t), bias);
+    (i ? r.y : r.x) = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return r;
+}
+
+struct TcArgs {
+  TreeArgs t;
+  int G, tq;       // tq = 128 / G tokens of a row tile
+  int box;         // keys of a page piece
+  float* records;  // [blocks][2][D + 2][rows]: value sums, maximum, sum
+  Cut* cuts;
+};
+
+template <int D, int NT, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+               const __grid_constant__ CUtensorMap vmap, const TcArgs ta) {
+  using S = Shape<D, NT>;
+  constexpr bool kTwoTerms = std::is_same<T, __half>::value;
+  const TreeArgs& a = ta.t;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + S::off_bar);   // [stages] tx
+  uint64_t* raw_empty = raw_full + S::stages;   // [stages] converters
+  uint64_t* valid = raw_empty + S::stages;      // [stages][2] bits of the keys that a K tile holds
+  uint64_t* k_ready = valid + 2 * S::stages;    // converters
+  uint64_t* k_free = k_ready + 1;               // MMA commit
+  uint64_t* v_ready = k_free + 1;               // [2] converters
+  uint64_t* v_free = v_ready + 2;               // [2] MMA commit
+  uint64_t* q_full = v_free + 2;                // tx
+  uint64_t* q_free = q_full + 1;                // MMA commit
+  uint64_t* s_full = q_free + 1;                // [2] MMA commit
+  uint64_t* p_ready = s_full + 2;               // [2][2] 4 softmax warps: weights of the first, second 64 keys
+  uint64_t* pv_done = p_ready + 4;              // [2] MMA commit
+  uint64_t* done = pv_done + 2;
+  int64_t* scratch = reinterpret_cast<int64_t*>(done + 1);                // [2 + 20]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 22);
+  static_assert((4 * S::stages + 17 + 22) * 8 + 4 <= kBarBytes && S::bytes <= 232448, "shared memory");
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::stages; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], kConverters);
+    }
+    mbar_init(k_ready, kConverters);
+    mbar_init(k_free, 1);
+    mbar_init(q_full, 1);
+    mbar_init(q_free, 1);
+    mbar_init(done, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&v_ready[x], kConverters);
+      mbar_init(&v_free[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_ready[2 * x], 4);
+      mbar_init(&p_ready[2 * x + 1], 4);
+      mbar_init(&pv_done[x], 1);
+    }
+    fence_mbar_init();
+  }
+  // rows of a block in whole tokens: what seq_of counts blocks by
+  const int block_rows = NT * ta.tq * ta.G;
+  Walk<kTile> walk;
+  if (!range_of_block<kTile, kThreads>(a, block_rows, scratch, walk)) {
+    if (threadIdx.x == 0 && ta.cuts) ta.cuts[blockIdx.x].partial = 0;
+    return;
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Piece p;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 8) {
+      // ---------------- TMA
+      const int64_t pages = a.rows / a.page;
+      const int boxes = kTile / ta.box;
+      int x = 0, i = 0;
+      bool ok = true;
+      while (ok && walk.next(a, block_rows, p)) {
+        if (i > 0 && !mbar_wait_warp(q_free, (uint32_t)((i - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        ++i;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full, (uint32_t)(NT * S::slabs * ta.tq * ta.G * 128));
+          for (int t = 0; t < NT; ++t)
+            for (int sl = 0; sl < S::slabs; ++sl)
+              tma_load_3d(&qmap, q_full, smem + t * S::tile + sl * kTile * 128, sl * 64, p.h * ta.G,
+                          p.b * a.n + (p.rb * NT + t) * ta.tq);
+        }
+        const int32_t* table = a.block_table + ((int64_t)p.b * a.Hkv + p.h) * a.max_pages;
+        // lane i: piece i of a tile; its page id is read one tile ahead
+        auto row_of = [&](int tile) -> int {
+          const int t = tile * kTile + lane * ta.box;
+          if (lane >= boxes || tile >= p.hi || t >= p.s.T) return -1;
+          const int id = __ldg(table + t / a.page);
+          if (id < 0 || id >= pages) {
+            atomicOr(a.status, kStatusRange);
+            return -1;
+          }
+          return id * a.page + t % a.page;
+        };
+        int row = row_of(p.lo);
+        for (int tile = p.lo; ok && tile < p.hi; ++tile) {
+          const int next = row_of(tile + 1);
+          const uint32_t live = __ballot_sync(kFull, row >= 0);
+          for (int kv = 0; kv < 2; ++kv, ++x) {
+            const int s = x % S::stages;
+            if (!mbar_wait_warp(&raw_empty[s], (uint32_t)(((x / S::stages) & 1) ^ 1))) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              if (kv == 0) {
+                const int left = p.s.T - tile * kTile;
+                for (int half = 0; half < 2; ++half) {
+                  uint64_t bits = 0;
+                  for (int b = 0; b < boxes; ++b) {
+                    const int at = b * ta.box - half * 64;
+                    if ((live >> b & 1) && at >= 0 && at < 64) bits |= (ta.box == 64 ? ~0ull : (1ull << ta.box) - 1) << at;
+                  }
+                  const int here = left - half * 64;
+                  if (here < 64) bits &= here <= 0 ? 0ull : (1ull << here) - 1;
+                  valid[2 * s + half] = bits;
+                }
+              }
+              mbar_arrive_expect_tx(&raw_full[s], (uint32_t)(__popc(live) * ta.box * (D + (kv ? 0 : 8))));
+            }
+            __syncwarp();
+            if (row >= 0) {
+              tma_load_2d(kv ? &vmap : &kmap, &raw_full[s], smem + S::off_raw + s * S::raw + lane * ta.box * D, 0, row);
+              if (kv == 0) {
+                uint8_t* sc = smem + S::off_rs + s * S::scales + lane * ta.box * 4;
+                bulk_load(sc, a.kscales + row, ta.box * 4, &raw_full[s]);
+                bulk_load(sc + kTile * 4, a.vscales + row, ta.box * 4, &raw_full[s]);
+              }
+            }
+          }
+          row = next;
+        }
+      }
+      if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
+      // no copy may still be in flight when the block ends
+      if (lane == 0) {
+        for (int y = x > S::stages ? x - S::stages : 0; y < x; ++y)
+          if (!mbar_wait(&raw_full[y % S::stages], (uint32_t)((y / S::stages) & 1))) atomicOr(a.status, kStatusTimeout);
+        if (i > 0 && !mbar_wait(q_full, (uint32_t)((i - 1) & 1))) atomicOr(a.status, kStatusTimeout);
+      }
+    } else if (warp == 9) {
+      // ---------------- MMA
+      constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+      constexpr uint32_t idesc_s = idesc_f16(kTile, kTile, bf), idesc_o = idesc_f16(kTile, D, true) | (1u << 16);
+      const uint32_t lead = elect_one();
+      const uint64_t qd = sw128_kmajor_desc(smem_u32(smem)), kd = sw128_kmajor_desc(smem_u32(smem + S::off_k));
+      const uint64_t vd = sw128_mnmajor_desc(smem_u32(smem + S::off_v), kTile * 128);
+      int kt = 0, i = 0, pv[2] = {0, 0};                    // tiles, items, value products of row tiles so far
+      bool ok = true;
+      auto logits = [&](int t, int n) -> bool {             // the buffer's last weights must have been consumed
+        if (n > 0 && !mbar_wait_warp(&pv_done[t], (uint32_t)((n - 1) & 1))) return false;
+        tc_fence_after();
+        const uint64_t q = qd + t * (S::tile >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (uint32_t)((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4;
+          mma_ss(tmem + kColS + t * 128, q + off, kd + off, idesc_s, ks ? 1u : 0u, lead);
+        }
+        commit(&s_full[t], lead);
+        return true;
+      };
+      auto values = [&](int t, int n, int buf, bool first) -> bool {
+        const uint64_t v = vd + buf * (S::tile >> 4);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!mbar_wait_warp(&p_ready[2 * t + hf], (uint32_t)(n & 1))) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint32_t pc = tmem + kColS + t * 128 + 64 * hf + 8 * ks;
+            const uint64_t vk = v + (4 * hf + ks) * (2048 >> 4);
+            mma_ts(tmem + kColO + t * 128, pc, vk, idesc_o, (first && hf == 0 && ks == 0) ? 0u : 1u, lead);
+            if constexpr (kTwoTerms) mma_ts(tmem + kColO + t * 128, pc + 32, vk, idesc_o, 1u, lead);
+          }
+        }
+        commit(&pv_done[t], lead);
+        return true;
+      };
+      while (ok && walk.next(a, block_rows, p)) {
+        const bool two = NT == 2 && (p.rb * NT + 1) * ta.tq < p.s.drafts;
+        ok = mbar_wait_warp(q_full, (uint32_t)(i++ & 1)) && mbar_wait_warp(k_ready, (uint32_t)(kt & 1)) && logits(0, pv[0]) &&
+             (!two || logits(1, pv[1]));
+        if (!ok) break;
+        commit(k_free, lead);
+        if (p.hi - p.lo == 1) commit(q_free, lead);
+        for (int tile = p.lo; tile < p.hi; ++tile, ++kt) {
+          const int buf = kt & 1;
+          const bool more = tile + 1 < p.hi;
+          if (!(ok = mbar_wait_warp(&v_ready[buf], (uint32_t)((kt >> 1) & 1)))) break;
+          if (!(ok = values(0, pv[0]++, buf, tile == p.lo))) break;
+          if (more && !(ok = mbar_wait_warp(k_ready, (uint32_t)((kt + 1) & 1)) && logits(0, pv[0]))) break;
+          if (two && !(ok = values(1, pv[1]++, buf, tile == p.lo))) break;
+          commit(&v_free[buf], lead);
+          if (more && two && !(ok = logits(1, pv[1]))) break;
+          if (more) commit(k_free, lead);
+          if (tile + 2 == p.hi) commit(q_free, lead);
+        }
+      }
+      if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
+      // nothing may still run when tensor memory is given back
+      commit(done, lead);
+      if (!mbar_wait_warp(done, 0) && lane == 0) atomicOr(a.status, kStatusTimeout);
+    } else if (warp >= 12) {
+      // ---------------- converters
+      const int w = warp - 12;
+      constexpr int kPer = D / 16;                          // 16-byte pieces of a key's codes
+      constexpr int kKeysPerWarp = 32 / kPer;
+      const int u = lane % kPer, sub = lane / kPer;
+      int x = 0, kt = 0;
+      bool ok = true;
+      auto convert = [&](const uint8_t* raw, uint8_t* dst, auto type) {
+#pragma unroll 2
+        for (int k0 = w * kKeysPerWarp; k0 < kTile; k0 += kConverters * kKeysPerWarp) {
+          const int key = k0 + sub;
+          const uint4 c = *reinterpret_cast<const uint4*>(raw + key * D + u * 16);
+          const uint2 e0 = codes4(c.x, type), e1 = codes4(c.y, type), e2 = codes4(c.z, type), e3 = codes4(c.w, type);
+          // 64 coordinates a slab, the second half of a row in the other slab: its
+          // lanes store their two chunks in the other order, off the first's banks
+          uint8_t* rowp = dst + (u >> 2) * kTile * 128 + key * 128;
+          const int c0 = 2 * (u & 3), flip = u >> 2;
+          const uint4 lo = make_uint4(e0.x, e0.y, e1.x, e1.y), hi = make_uint4(e2.x, e2.y, e3.x, e3.y);
+          *reinterpret_cast<uint4*>(rowp + (((c0 + flip) ^ (key & 7)) << 4)) = flip ? hi : lo;
+          *reinterpret_cast<uint4*>(rowp + (((c0 + (flip ^ 1)) ^ (key & 7)) << 4)) = flip ? lo : hi;
+        }
+      };
+      while (ok && walk.next(a, block_rows, p)) {
+        for (int tile = p.lo; ok && tile < p.hi; ++tile, ++kt) {
+          for (int kv = 0; kv < 2; ++kv, ++x) {
+            const int s = x % S::stages, buf = kt & 1;
+            const uint8_t* raw = smem + S::off_raw + s * S::raw;
+            ok = mbar_wait_warp(&raw_full[s], (uint32_t)((x / S::stages) & 1)) &&
+                 (kv ? kt < 2 || mbar_wait_warp(&v_free[buf], (uint32_t)(((kt >> 1) - 1) & 1))
+                     : kt < 1 || mbar_wait_warp(k_free, (uint32_t)((kt - 1) & 1)));
+            if (!ok) break;
+            if (kv == 0) {
+              convert(raw, smem + S::off_k, T());
+              if (w < 4) {
+                const int key = w * 32 + lane;
+                const float* rs = reinterpret_cast<const float*>(smem + S::off_rs + s * S::scales);
+                float* sc = reinterpret_cast<float*>(smem + S::off_sc + buf * S::scales);
+                const uint32_t bits = (uint32_t)(valid[2 * s + (w >> 1)] >> (32 * (w & 1)));
+                const bool there = bits >> lane & 1;
+                sc[key] = there ? rs[key] * a.scale_log2 : 0.f;
+                sc[kTile + key] = there ? rs[kTile + key] : 0.f;
+                if (lane == 0) reinterpret_cast<uint32_t*>(smem + S::off_valid)[buf * 4 + w] = bits;
+              }
+            } else {
+              convert(raw, smem + S::off_v + buf * S::tile, __nv_bfloat16());
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(kv ? &v_ready[buf] : k_ready);
+              mbar_arrive(&raw_empty[s]);
+            }
+          }
+        }
+      }
+      if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
+    }
+  } else {
+    // ---------------- softmax: thread = row of tile t
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t sc = tmem + lanes + kColS + t * 128, oc = tmem + lanes + kColO + t * 128;
+    const int row_tok = r / ta.G, row_head = r % ta.G;
+    const int words = (a.n + 31) / 32;
+    int kt = 0, steps = 0, kept = 0;
+    bool ok = true;
+    while (ok && t < NT && walk.next(a, block_rows, p)) {
+      const int tok = (p.rb * NT + t) * ta.tq + row_tok;
+      if (t && (p.rb * NT + t) * ta.tq >= p.s.drafts) {     // no rows here
+        kt += p.hi - p.lo;
+        continue;
+      }
+      const bool live = row_tok < ta.tq && tok < p.s.drafts;
+      float m = -INFINITY, l = 0.f;
+      for (int tile = p.lo; tile < p.hi; ++tile, ++kt, ++steps) {
+        if (!(ok = mbar_wait_warp(&s_full[t], (uint32_t)(steps & 1)))) break;
+        tc_fence_after();
+        const float4* kscale = reinterpret_cast<const float4*>(smem + S::off_sc + (kt & 1) * S::scales);
+        const float4* vscale = kscale + kTile / 4;
+        const int t0 = tile * kTile;
+        // which keys the row sees: those that are there, and of the drafted ones its own
+        uint32_t sees[4];
+        bool whole = t0 + kTile <= p.s.ctx;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          sees[c] = reinterpret_cast<const uint32_t*>(smem + S::off_valid)[(kt & 1) * 4 + c];
+          whole = whole && sees[c] == kFull;
+        }
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int j = t0 + 32 * c - p.s.ctx;            // the group's first key among the drafted ones
+            if (j + 31 < 0) continue;
+            uint32_t bits = 0;
+            if (live) {
+              if (a.mask) {
+                const uint32_t* mk = a.mask + ((int64_t)p.b * a.n + tok) * words;
+                const int w0 = j < 0 ? 0 : j >> 5;
+                const uint32_t lo = w0 < words ? __ldg(mk + w0) : 0u, hi = w0 + 1 < words ? __ldg(mk + w0 + 1) : 0u;
+                bits = j < 0 ? lo << -j : __funnelshift_r(lo, hi, j & 31);
+              } else {
+                const int upto = tok - j;                   // the last drafted key it sees, from the group's first
+                bits = upto < 0 ? 0u : upto >= 31 ? kFull : (2u << upto) - 1;
+              }
+            }
+            if (j < 0) bits |= (1u << -j) - 1;              // context
+            sees[c] &= bits;
+          }
+        }
+        // first reading: the row's largest logit (base 2)
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float x[32];
+          tmem_ld32(sc + 32 * c, x);
+          tmem_wait_ld();
+          regs_after_wait(x);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 k = kscale[8 * c + e / 4];
+            x[e] *= k.x, x[e + 1] *= k.y, x[e + 2] *= k.z, x[e + 3] *= k.w;
+          }
+          if (!whole) {
+            const uint32_t b = c == 0 ? sees[0] : c == 1 ? sees[1] : c == 2 ? sees[2] : sees[3];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = b >> e & 1 ? x[e] : -INFINITY;
+          }
+          float mx[2] = {x[0], x[1]};
+#pragma unroll
+          for (int e = 2; e < 32; e += 4) {
+            mx[0] = max3(mx[0], x[e], x[e + 1]);
+            if (e + 3 < 32) mx[1] = max3(mx[1], x[e + 2], x[e + 3]);
+          }
+          top = max3(top, mx[0], mx[1]);
+        }
+        if (!(top < INFINITY)) l = NAN;                     // a seen logit is NaN or infinite: so is the row
+        const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
+        if (__any_sync(kFull, grow)) {
+          float f = 1.f;
+          if (grow) {
+            f = m == -INFINITY ? 0.f : ex2(m - top);
+            l *= f;
+            m = top;
+          }
+          if (tile > p.lo) {
+            // the value product of the tile before was done before these logits began
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              tmem_ld16(oc + c, o);
+              tmem_wait_ld();
+              uint32_t y[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                asm volatile("" : "+f"(o[e])::"memory");
+                y[e] = __float_as_uint(f == 0.f ? 0.f : o[e] * f);
+              }
+              tmem_st16(oc + c, y);
+            }
+          }
+        }
+        // second reading: the weights, in place
+        const float ref = m == -INFINITY ? 0.f : m;
+        float sum[2] = {0.f, 0.f};
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t z[2][kTwoTerms ? 16 : 1];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = 2 * hf + h;
+            float x[32];
+            uint32_t y[16];
+            tmem_ld32(sc + 32 * c, x);
+            tmem_wait_ld();
+            regs_after_wait(x);
+            const uint32_t b = hf ? sees[2 + h] : sees[h];
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 k = kscale[8 * c + e / 4], v = vscale[8 * c + e / 4];
+              const float ks[4] = {k.x, k.y, k.z, k.w}, vs[4] = {v.x, v.y, v.z, v.w};
+              float wt[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float pw = ex2(fmaf(x[e + i], ks[i], -ref));
+                wt[i] = pw * vs[i];
+                if (!whole && !(b >> (e + i) & 1)) pw = wt[i] = 0.f;   // 0 times whatever an unseen key's scale is
+                sum[i & 1] += pw;
+              }
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) {
+                y[(e + i) / 2] = pack_bf16(wt[i], wt[i + 1]);
+                if constexpr (kTwoTerms) z[h][(e + i) / 2] = pack_rest(wt[i], wt[i + 1], y[(e + i) / 2]);
+              }
+            }
+            tmem_st16(sc + 64 * hf + 16 * h, y);
+          }
+          // over logits that have all been read by now
+          if constexpr (kTwoTerms) {
+            tmem_st16(sc + 64 * hf + 32, z[0]);
+            tmem_st16(sc + 64 * hf + 48, z[1]);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[2 * t + hf]);
+        }
+        l += sum[0] + sum[1];
+      }
+      if (!ok) break;
+      if (!(ok = mbar_wait_warp(&pv_done[t], (uint32_t)((steps - 1) & 1)))) break;
+      tc_fence_after();
+      const bool all = p.lo == 0 && p.hi == p.s.tiles;
+      if (!all && p.lo > 0 && threadIdx.x == 0) {
+        ta.cuts[blockIdx.x] = Cut{p.begin, p.begin + p.s.tiles, p.b, p.h, p.rb, 1};
+        kept = 1;
+      }
+      float* rec = all ? nullptr
+                       : ta.records + ((int64_t)blockIdx.x * 2 + (p.lo > 0 ? 0 : 1)) * (D + 2) * S::rows + t * kTile + r;
+      const int64_t row = ((int64_t)p.b * a.n + tok) * a.Hq + p.h * ta.G + row_head;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_ld32(oc + c, o);
+        tmem_wait_ld();
+        regs_after_wait(o);
+        if (all) {
+          if (live) {
+            T* out = static_cast<T*>(a.out) + row * a.d + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              if (c + e < a.d)
+                *reinterpret_cast<uint4*>(out + e) =
+                    make_uint4(pack(o[e] * inv, o[e + 1] * inv, T()), pack(o[e + 2] * inv, o[e + 3] * inv, T()),
+                               pack(o[e + 4] * inv, o[e + 5] * inv, T()), pack(o[e + 6] * inv, o[e + 7] * inv, T()));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) rec[(int64_t)(c + e) * S::rows] = o[e];   // a column of rows at a time
+        }
+      }
+      if (all) {
+        if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      } else {
+        rec[(int64_t)D * S::rows] = m;
+        rec[(int64_t)(D + 1) * S::rows] = l;
+      }
+      tc_fence_before();
+    }
+    if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
+    if (threadIdx.x == 0 && ta.cuts && !kept) ta.cuts[blockIdx.x].partial = 0;
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the item that the main grid's block i (> 0) began inside of, if
+// i is the item's first cut: the second record of block i - 1 and the first ones of
+// i, i + 1, ..  Thread = row; blockIdx.y takes 16 of the coordinates.
+template <int D, int NT, typename T>
+__global__ void __launch_bounds__(NT * kTile) tree_tc_merge_kernel(const TcArgs ta, int grid) {
+  using S = Shape<D, NT>;
+  const TreeArgs& a = ta.t;
+  const int i = blockIdx.x + 1;
+  const Cut cut = ta.cuts[i];
+  if (!cut.partial) return;
+  __shared__ int64_t part[NT * 4];
+  const int block_rows = NT * ta.tq * ta.G;
+  int64_t sum = 0;
+  for (int b = threadIdx.x; b < a.B; b += NT * kTile) sum += units_of(a, seq_of<kTile>(a, b, block_rows));
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  int64_t total = 0;
+  for (int w = 0; w < NT * 4; ++w) total += part[w];
+  int last;
+  if (!first_cut_of(cut, i, grid, total, last)) return;
+  const int t = threadIdx.x / kTile, row_tok = threadIdx.x % kTile / ta.G, row_head = threadIdx.x % kTile % ta.G;
+  const int tok = (cut.rb * NT + t) * ta.tq + row_tok;
+  const int drafts = a.draft_lens ? min(max(__ldg(a.draft_lens + cut.b), 0), a.n) : a.n;
+  if (row_tok >= ta.tq || tok >= drafts) return;
+  auto rec = [&](int x) { return ta.records + ((int64_t)x * 2 + (x == i - 1 ? 1 : 0)) * (D + 2) * S::rows + threadIdx.x; };
+  float m = -INFINITY;
+  for (int x = i - 1; x <= last; ++x) m = fmaxf(m, rec(x)[(int64_t)D * S::rows]);
+  float l = 0.f, v[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = 0.f;
+  for (int x = i - 1; x <= last; ++x) {
+    const float* p = rec(x);
+    const float mx = p[(int64_t)D * S::rows], lx = p[(int64_t)(D + 1) * S::rows];
+    if (mx == -INFINITY) {
+      l += lx;                                              // 0, or NaN
+      continue;
+    }
+    const float f = ex2(mx - m);
+    l += lx * f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = fmaf(p[(int64_t)(blockIdx.y * 16 + e) * S::rows], f, v[e]);
+  }
+  const int64_t row = ((int64_t)cut.b * a.n + tok) * a.Hq + cut.h * ta.G + row_head;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* out = static_cast<T*>(a.out) + row * a.d + blockIdx.y * 16;
+  if ((int)blockIdx.y * 16 < a.d) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 8)
+      *reinterpret_cast<uint4*>(out + e) =
+          make_uint4(pack(v[e] * inv, v[e + 1] * inv, T()), pack(v[e + 2] * inv, v[e + 3] * inv, T()),
+                     pack(v[e + 4] * inv, v[e + 5] * inv, T()), pack(v[e + 6] * inv, v[e + 7] * inv, T()));
+  }
+  if (a.lse && blockIdx.y == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// raw rows of one page piece, unswizzled
+bool raw_map(CUtensorMap* m, const int8_t* base, int d, int64_t rows, int box) {
+  const EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)d};
+  cuuint32_t boxd[2] = {(cuuint32_t)(d <= 64 ? 64 : 128), (cuuint32_t)box};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides, boxd, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NT, typename T>
+int launch_shape(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, TcArgs ta, int grid, bool merge,
+                 void* workspace, cudaStream_t st) {
+  using S = Shape<D, NT>;
+  const int e = ensure_dyn_smem(reinterpret_cast<const void*>(tree_tc_kernel<D, NT, T>), S::bytes);
+  if (e) return e;
+  if (merge) {
+    ta.cuts = static_cast<Cut*>(workspace);
+    ta.records = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((size_t)grid * sizeof(Cut) + 255) / 256 * 256);
+  }
+  tree_tc_kernel<D, NT, T><<<grid, kThreads, S::bytes, st>>>(qm, km, vm, ta);
+  const int e2 = (int)cudaGetLastError();
+  if (e2 || !merge) return e2;
+  tree_tc_merge_kernel<D, NT, T><<<dim3(grid - 1, D / 16), NT * kTile, 0, st>>>(ta, grid);
+  return (int)cudaGetLastError();
+}
+
+int row_tiles(int64_t rows) { return rows <= kTile ? 1 : 2; }
+
+}  // namespace
+
+bool tree_tc_supported(const tq_ctx* h, int n, int Hq, int Hkv) {
+  const int64_t G = Hq / Hkv;
+  return h->d <= 128 && G <= kTile && n * G > kTreeTcRows;
+}
+
+size_t tree_tc_workspace(const tq_ctx* h, int n, int Hq, int Hkv) {
+  const size_t grid = h->sm_count, rows = (size_t)row_tiles((int64_t)n * (Hq / Hkv)) * kTile;
+  return (grid * sizeof(Cut) + 255) / 256 * 256 + grid * 2 * ((h->d <= 64 ? 64 : 128) + 2) * rows * 4;
+}
+
+int launch_tree_tc(const tq_ctx* h, const TreeArgs& a, int dtype, void* workspace, void* stream) {
+  TcArgs ta{};
+  ta.t = a;
+  ta.G = a.Hq / a.Hkv, ta.tq = kTile / ta.G;
+  ta.box = 64;
+  while (a.page % ta.box) ta.box /= 2;   // page pieces that a tile never splits
+  const bool bf = dtype == TQ_BF16;
+  CUtensorMap qm, km, vm;
+  const int64_t tokens = (int64_t)a.B * a.n;
+  if (!token_map(&qm, a.q, bf, h->d, a.Hq, tokens, tokens > 1 ? a.q_stride : (int64_t)a.Hq * h->d, ta.G, ta.tq) ||
+      !raw_map(&km, a.kcodes, h->d, a.rows, ta.box) || !raw_map(&vm, a.vcodes, h->d, a.rows, ta.box))
+    return (int)cudaErrorInvalidValue;
+  const int nt = row_tiles((int64_t)a.n * ta.G);
+  const int64_t blocks = (a.n + nt * ta.tq - 1) / (nt * ta.tq), tiles = ((int64_t)a.max_pages * a.page + kTile - 1) / kTile;
+  const int64_t items = (int64_t)a.B * a.Hkv * blocks;
+  const int grid = (int)(items >= h->sm_count || tiles >= h->sm_count ? h->sm_count : std::min<int64_t>(h->sm_count, items * tiles));
+  const bool merge = tiles > 1 && grid > 1;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define TQ_TREE(D, NT)                                                                       \
+  return bf ? launch_shape<D, NT, __nv_bfloat16>(qm, km, vm, ta, grid, merge, workspace, st) \
+            : launch_shape<D, NT, __half>(qm, km, vm, ta, grid, merge, workspace, st)
+  if (h->d <= 64) {
+    if (nt == 1) TQ_TREE(64, 1);
+    TQ_TREE(64, 2);
+  }
+  if (nt == 1) TQ_TREE(128, 1);
+  TQ_TREE(128, 2);
+#undef TQ_TREE
+}
+
+}  // namespace tqi
