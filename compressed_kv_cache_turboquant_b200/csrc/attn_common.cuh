@@ -17,6 +17,19 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;   // a row's reference moves when a logit passes it by 2^8
 
+// Bounded waits as mbar_wait's, in a few instructions: the limit counts tries, each
+// of which sleeps up to 200 us of device time, instead of reading the timer.  These
+// kernels wait in some thirty places, and their warps' different loops have to
+// share the instruction cache.
+constexpr int kWaitTries = 1 << 15;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < kWaitTries; ++i)
+    if (mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
+  return false;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)); }
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

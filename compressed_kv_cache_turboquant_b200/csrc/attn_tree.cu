@@ -198,7 +198,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
       for (int tile = p.lo; tile < p.hi; ++tile, ++it) {
         const int s = it % S::stages;
         const int next = row_of(tile + 1);
-        if (!mbar_wait_warp(&empty[s], (uint32_t)(((it / S::stages) & 1) ^ 1))) {
+        if (!wait_warp(&empty[s], (uint32_t)(((it / S::stages) & 1) ^ 1))) {
           ok = false;
           break;
         }
@@ -233,7 +233,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
       if (lane == 0) atomicOr(a.status, kStatusTimeout);
       // no copy may still be in flight when the block ends
       for (int i = it > S::stages ? it - S::stages : 0; i < it; ++i)
-        mbar_wait(&full[i % S::stages], (uint32_t)((i / S::stages) & 1));
+        wait(&full[i % S::stages], (uint32_t)((i / S::stages) & 1));
     }
     return;
   }
@@ -323,7 +323,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 
     for (int tile = p.lo; tile < p.hi; ++tile, ++it) {
       const int s = it % S::stages;
-      if (ok) ok = mbar_wait_warp(&full[s], (uint32_t)((it / S::stages) & 1));
+      if (ok) ok = wait_warp(&full[s], (uint32_t)((it / S::stages) & 1));
       if (!ok) continue;
       const uint32_t st = ring + s * S::stage;
       const uint32_t there = (uint32_t)(valid[s] >> (warp * 16)) & 0xFFFFu;

@@ -9,16 +9,23 @@
 // block; queries enter as they are.  Against attn_tree.cu's blocks of 32 rows
 // the codes of a key tile are converted once for up to 256 rows.
 //
+// With one row tile its key tiles go to two streams in turn, each with its own
+// logits, weights, value sums and softmax, joined at the end of a piece: one's
+// softmax runs beside the other's products.  With two row tiles they are the two
+// streams.
+//
 // Warps (640 threads, one block per SM, persistent over equal ranges of 128-key
 // tiles; what a cut divides is joined by tree_tc_merge_kernel):
-//   0-3, 4-7  softmax of row tile 0, 1: thread = row (TMEM lane), a tile's logits
-//             read twice from tensor memory (maximum; weights, written over them)
+//   0-3, 4-7  softmax of stream 0, 1: thread = row (TMEM lane); a
+//             tile's logits are read twice, 32 keys at a time (maximum; weights),
+//             in loops that stay small: unrolled over the 128 keys they miss the
+//             instruction cache (7000 cycles a tile)
 //   8         TMA of the item's queries and of raw code tiles, a page piece at a
 //             time, K and V alternating in a ring
 //   9         the MMA issuer
 //   12-19     converters: raw codes -> swizzled 16-bit operand tiles (one K tile,
 //             two V tiles), scales and the bits of the keys that are there
-// Tensor memory: S/P of tiles 0, 1 at 0, 128; O at 256, 384.  The weights of the
+// Tensor memory: S/P of streams 0, 1 at 0, 128; O at 256, 384.  The weights of the
 // first 64 keys take 32 columns from the start of their tile's S, those of the
 // other 64 from its middle, and remainders follow each.
 #include <cuda_bf16.h>
@@ -55,9 +62,10 @@ struct Shape {
   static constexpr int off_v = off_k + tile;
   static constexpr int off_raw = off_v + 2 * tile;
   static constexpr int off_rs = off_raw + stages * raw;          // [stages][scales]
-  static constexpr int off_sc = off_rs + stages * scales;        // [2 tiles in turn][K scales x logit scale, V scales][128]
-  static constexpr int off_valid = off_sc + 2 * scales;          // [2][4] words
-  static constexpr int off_bar = off_valid + 2 * 16;
+  static constexpr int off_sc = off_rs + stages * scales;        // [4 tiles in turn][K scales x logit scale, V scales][128]
+  static constexpr int off_valid = off_sc + 4 * scales;          // [4][4] words
+  static constexpr int off_swap = off_valid + 4 * 16;            // [2][128] maxima and sums of the second stream
+  static constexpr int off_bar = off_swap + 2 * kTile * 4;
   static constexpr int bytes = off_bar + kBarBytes + 1024;
   static constexpr int rows = NT * kTile;
 };
@@ -118,10 +126,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   uint64_t* s_full = q_free + 1;                // [2] MMA commit
   uint64_t* p_ready = s_full + 2;               // [2][2] 4 softmax warps: weights of the first, second 64 keys
   uint64_t* pv_done = p_ready + 4;              // [2] MMA commit
-  uint64_t* done = pv_done + 2;
+  uint64_t* x_ready = pv_done + 2;              // 4 warps of stream 1: its maxima and sums written, its values done
+  uint64_t* x_free = x_ready + 1;               // 4 warps of stream 0: they and its O read
+  uint64_t* done = x_free + 1;
   int64_t* scratch = reinterpret_cast<int64_t*>(done + 1);                // [2 + 20]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 22);
-  static_assert((4 * S::stages + 17 + 22) * 8 + 4 <= kBarBytes && S::bytes <= 232448, "shared memory");
+  static_assert((4 * S::stages + 19 + 22) * 8 + 4 <= kBarBytes && S::bytes <= 232448, "shared memory");
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::stages; ++s) {
@@ -132,6 +142,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     mbar_init(k_free, 1);
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
+    mbar_init(x_ready, 4);
+    mbar_init(x_free, 4);
     mbar_init(done, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&v_ready[x], kConverters);
@@ -166,7 +178,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       int x = 0, i = 0;
       bool ok = true;
       while (ok && walk.next(a, block_rows, p)) {
-        if (i > 0 && !mbar_wait_warp(q_free, (uint32_t)((i - 1) & 1))) {
+        if (i > 0 && !wait_warp(q_free, (uint32_t)((i - 1) & 1))) {
           ok = false;
           break;
         }
@@ -196,7 +208,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           const uint32_t live = __ballot_sync(kFull, row >= 0);
           for (int kv = 0; kv < 2; ++kv, ++x) {
             const int s = x % S::stages;
-            if (!mbar_wait_warp(&raw_empty[s], (uint32_t)(((x / S::stages) & 1) ^ 1))) {
+            if (!wait_warp(&raw_empty[s], (uint32_t)(((x / S::stages) & 1) ^ 1))) {
               ok = false;
               break;
             }
@@ -233,8 +245,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       // no copy may still be in flight when the block ends
       if (lane == 0) {
         for (int y = x > S::stages ? x - S::stages : 0; y < x; ++y)
-          if (!mbar_wait(&raw_full[y % S::stages], (uint32_t)((y / S::stages) & 1))) atomicOr(a.status, kStatusTimeout);
-        if (i > 0 && !mbar_wait(q_full, (uint32_t)((i - 1) & 1))) atomicOr(a.status, kStatusTimeout);
+          if (!wait(&raw_full[y % S::stages], (uint32_t)((y / S::stages) & 1))) atomicOr(a.status, kStatusTimeout);
+        if (i > 0 && !wait(q_full, (uint32_t)((i - 1) & 1))) atomicOr(a.status, kStatusTimeout);
       }
     } else if (warp == 9) {
       // ---------------- MMA
@@ -243,12 +255,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       const uint32_t lead = elect_one();
       const uint64_t qd = sw128_kmajor_desc(smem_u32(smem)), kd = sw128_kmajor_desc(smem_u32(smem + S::off_k));
       const uint64_t vd = sw128_mnmajor_desc(smem_u32(smem + S::off_v), kTile * 128);
-      int kt = 0, i = 0, pv[2] = {0, 0};                    // tiles, items, value products of row tiles so far
+      int kt = 0, i = 0, pv[2] = {0, 0};                    // tiles, items, value products of the streams so far
       bool ok = true;
-      auto logits = [&](int t, int n) -> bool {             // the buffer's last weights must have been consumed
-        if (n > 0 && !mbar_wait_warp(&pv_done[t], (uint32_t)((n - 1) & 1))) return false;
+      // stream t, queries of row tile qt; the buffer's last weights must have been consumed
+      auto logits = [&](int t, int qt, int n) -> bool {
+        if (n > 0 && !wait_warp(&pv_done[t], (uint32_t)((n - 1) & 1))) return false;
         tc_fence_after();
-        const uint64_t q = qd + t * (S::tile >> 4);
+        const uint64_t q = qd + qt * (S::tile >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = (uint32_t)((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4;
@@ -261,7 +274,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         const uint64_t v = vd + buf * (S::tile >> 4);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          if (!mbar_wait_warp(&p_ready[2 * t + hf], (uint32_t)(n & 1))) return false;
+          if (!wait_warp(&p_ready[2 * t + hf], (uint32_t)(n & 1))) return false;
           tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
@@ -276,28 +289,42 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       };
       while (ok && walk.next(a, block_rows, p)) {
         const bool two = NT == 2 && (p.rb * NT + 1) * ta.tq < p.s.drafts;
-        ok = mbar_wait_warp(q_full, (uint32_t)(i++ & 1)) && mbar_wait_warp(k_ready, (uint32_t)(kt & 1)) && logits(0, pv[0]) &&
-             (!two || logits(1, pv[1]));
+        ok = wait_warp(q_full, (uint32_t)(i++ & 1)) && wait_warp(k_ready, (uint32_t)(kt & 1)) && logits(0, 0, pv[0]) &&
+             (!two || logits(1, 1, pv[1]));
         if (!ok) break;
         commit(k_free, lead);
         if (p.hi - p.lo == 1) commit(q_free, lead);
         for (int tile = p.lo; tile < p.hi; ++tile, ++kt) {
           const int buf = kt & 1;
           const bool more = tile + 1 < p.hi;
-          if (!(ok = mbar_wait_warp(&v_ready[buf], (uint32_t)((kt >> 1) & 1)))) break;
-          if (!(ok = values(0, pv[0]++, buf, tile == p.lo))) break;
-          if (more && !(ok = mbar_wait_warp(k_ready, (uint32_t)((kt + 1) & 1)) && logits(0, pv[0]))) break;
-          if (two && !(ok = values(1, pv[1]++, buf, tile == p.lo))) break;
-          commit(&v_free[buf], lead);
-          if (more && two && !(ok = logits(1, pv[1]))) break;
-          if (more) commit(k_free, lead);
-          if (tile + 2 == p.hi) commit(q_free, lead);
+          if constexpr (NT == 1) {
+            // the next tile's logits go to the other stream, ahead of this one's values
+            const int t = (tile - p.lo) & 1;
+            if (more) {
+              if (!(ok = wait_warp(k_ready, (uint32_t)((kt + 1) & 1)) && logits(t ^ 1, 0, t ? pv[0] : pv[1]))) break;
+              commit(k_free, lead);
+              if (tile + 2 == p.hi) commit(q_free, lead);
+            }
+            if (!(ok = wait_warp(&v_ready[buf], (uint32_t)((kt >> 1) & 1)))) break;
+            if (!(ok = values(t, t ? pv[1] : pv[0], buf, tile - p.lo < 2))) break;
+            ++(t ? pv[1] : pv[0]);
+            commit(&v_free[buf], lead);
+          } else {
+            if (!(ok = wait_warp(&v_ready[buf], (uint32_t)((kt >> 1) & 1)))) break;
+            if (!(ok = values(0, pv[0]++, buf, tile == p.lo))) break;
+            if (more && !(ok = wait_warp(k_ready, (uint32_t)((kt + 1) & 1)) && logits(0, 0, pv[0]))) break;
+            if (two && !(ok = values(1, pv[1]++, buf, tile == p.lo))) break;
+            commit(&v_free[buf], lead);
+            if (more && two && !(ok = logits(1, 1, pv[1]))) break;
+            if (more) commit(k_free, lead);
+            if (tile + 2 == p.hi) commit(q_free, lead);
+          }
         }
       }
       if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
       // nothing may still run when tensor memory is given back
       commit(done, lead);
-      if (!mbar_wait_warp(done, 0) && lane == 0) atomicOr(a.status, kStatusTimeout);
+      if (!wait_warp(done, 0) && lane == 0) atomicOr(a.status, kStatusTimeout);
     } else if (warp >= 12) {
       // ---------------- converters
       const int w = warp - 12;
@@ -326,24 +353,28 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           for (int kv = 0; kv < 2; ++kv, ++x) {
             const int s = x % S::stages, buf = kt & 1;
             const uint8_t* raw = smem + S::off_raw + s * S::raw;
-            ok = mbar_wait_warp(&raw_full[s], (uint32_t)((x / S::stages) & 1)) &&
-                 (kv ? kt < 2 || mbar_wait_warp(&v_free[buf], (uint32_t)(((kt >> 1) - 1) & 1))
-                     : kt < 1 || mbar_wait_warp(k_free, (uint32_t)((kt - 1) & 1)));
+            ok = wait_warp(&raw_full[s], (uint32_t)((x / S::stages) & 1)) &&
+                 (kv ? kt < 2 || wait_warp(&v_free[buf], (uint32_t)(((kt >> 1) - 1) & 1))
+                     : kt < 1 || wait_warp(k_free, (uint32_t)((kt - 1) & 1)));
             if (!ok) break;
+            uint8_t* dst = smem + (kv ? S::off_v + buf * S::tile : S::off_k);
+            if constexpr (kTwoTerms) {
+              if (kv) convert(raw, dst, __nv_bfloat16());
+              else convert(raw, dst, T());
+            } else {
+              convert(raw, dst, T());
+            }
             if (kv == 0) {
-              convert(raw, smem + S::off_k, T());
               if (w < 4) {
                 const int key = w * 32 + lane;
                 const float* rs = reinterpret_cast<const float*>(smem + S::off_rs + s * S::scales);
-                float* sc = reinterpret_cast<float*>(smem + S::off_sc + buf * S::scales);
+                float* sc = reinterpret_cast<float*>(smem + S::off_sc + (kt & 3) * S::scales);
                 const uint32_t bits = (uint32_t)(valid[2 * s + (w >> 1)] >> (32 * (w & 1)));
                 const bool there = bits >> lane & 1;
                 sc[key] = there ? rs[key] * a.scale_log2 : 0.f;
                 sc[kTile + key] = there ? rs[kTile + key] : 0.f;
-                if (lane == 0) reinterpret_cast<uint32_t*>(smem + S::off_valid)[buf * 4 + w] = bits;
+                if (lane == 0) reinterpret_cast<uint32_t*>(smem + S::off_valid)[(kt & 3) * 4 + w] = bits;
               }
-            } else {
-              convert(raw, smem + S::off_v + buf * S::tile, __nv_bfloat16());
             }
             fence_async_smem();
             __syncwarp();
@@ -357,27 +388,31 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
     }
   } else {
-    // ---------------- softmax: thread = row of tile t
+    // ---------------- softmax of stream t: thread = row of its row tile
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int t = warp >> 2, rt = NT == 2 ? t : 0, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t sc = tmem + lanes + kColS + t * 128, oc = tmem + lanes + kColO + t * 128;
     const int row_tok = r / ta.G, row_head = r % ta.G;
     const int words = (a.n + 31) / 32;
-    int kt = 0, steps = 0, kept = 0;
+    float* swap = reinterpret_cast<float*>(smem + S::off_swap) + r;
+    int kt0 = 0, steps = 0, kept = 0, joined = 0;           // tiles before this piece; steps of the stream; pieces of two streams
     bool ok = true;
-    while (ok && t < NT && walk.next(a, block_rows, p)) {
-      const int tok = (p.rb * NT + t) * ta.tq + row_tok;
-      if (t && (p.rb * NT + t) * ta.tq >= p.s.drafts) {     // no rows here
-        kt += p.hi - p.lo;
-        continue;
-      }
+    while (ok && walk.next(a, block_rows, p)) {
+      const int first = NT == 1 ? p.lo + t : p.lo, by = NT == 1 ? 2 : 1, base = kt0 - p.lo;
+      kt0 += p.hi - p.lo;
+      if (first >= p.hi || (p.rb * NT + rt) * ta.tq >= p.s.drafts) continue;   // no tiles, or no rows
+      const bool join = NT == 1 && p.hi - p.lo > 1;
+      // stream 0 has taken the last piece's sums
+      if (join && t == 1 && joined > 0 && !(ok = wait_warp(x_free, (uint32_t)((joined - 1) & 1)))) break;
+      const int tok = (p.rb * NT + rt) * ta.tq + row_tok;
       const bool live = row_tok < ta.tq && tok < p.s.drafts;
       float m = -INFINITY, l = 0.f;
-      for (int tile = p.lo; tile < p.hi; ++tile, ++kt, ++steps) {
-        if (!(ok = mbar_wait_warp(&s_full[t], (uint32_t)(steps & 1)))) break;
+      for (int tile = first; tile < p.hi; tile += by, ++steps) {
+        if (!(ok = wait_warp(&s_full[t], (uint32_t)(steps & 1)))) break;
         tc_fence_after();
-        const float4* kscale = reinterpret_cast<const float4*>(smem + S::off_sc + (kt & 1) * S::scales);
+        const int slot = (base + tile) & 3;
+        const float4* kscale = reinterpret_cast<const float4*>(smem + S::off_sc + slot * S::scales);
         const float4* vscale = kscale + kTile / 4;
         const int t0 = tile * kTile;
         // which keys the row sees: those that are there, and of the drafted ones its own
@@ -385,7 +420,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         bool whole = t0 + kTile <= p.s.ctx;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          sees[c] = reinterpret_cast<const uint32_t*>(smem + S::off_valid)[(kt & 1) * 4 + c];
+          sees[c] = reinterpret_cast<const uint32_t*>(smem + S::off_valid)[slot * 4 + c];
           whole = whole && sees[c] == kFull;
         }
         if (!whole) {
@@ -409,7 +444,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             sees[c] &= bits;
           }
         }
-        // first reading: the row's largest logit (base 2)
         float top = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -423,17 +457,17 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             x[e] *= k.x, x[e + 1] *= k.y, x[e + 2] *= k.z, x[e + 3] *= k.w;
           }
           if (!whole) {
-            const uint32_t b = c == 0 ? sees[0] : c == 1 ? sees[1] : c == 2 ? sees[2] : sees[3];
+            const uint32_t b = c < 2 ? (c ? sees[1] : sees[0]) : (c == 2 ? sees[2] : sees[3]);
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = b >> e & 1 ? x[e] : -INFINITY;
           }
           float mx[2] = {x[0], x[1]};
 #pragma unroll
-          for (int e = 2; e < 32; e += 4) {
+          for (int e = 2; e < 30; e += 4) {
             mx[0] = max3(mx[0], x[e], x[e + 1]);
-            if (e + 3 < 32) mx[1] = max3(mx[1], x[e + 2], x[e + 3]);
+            mx[1] = max3(mx[1], x[e + 2], x[e + 3]);
           }
-          top = max3(top, mx[0], mx[1]);
+          top = max3(top, max3(mx[0], x[30], x[31]), mx[1]);
         }
         if (!(top < INFINITY)) l = NAN;                     // a seen logit is NaN or infinite: so is the row
         const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
@@ -444,8 +478,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             l *= f;
             m = top;
           }
-          if (tile > p.lo) {
-            // the value product of the tile before was done before these logits began
+          if (tile > first) {
+            // the stream's value product before was done before these logits began
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               float o[16];
@@ -461,71 +495,111 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             }
           }
         }
-        // second reading: the weights, in place
         const float ref = m == -INFINITY ? 0.f : m;
         float sum[2] = {0.f, 0.f};
+        uint32_t rest[kTwoTerms ? 16 : 1];                  // remainders of the first group of a half
 #pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t z[2][kTwoTerms ? 16 : 1];
+        for (int c = 0; c < 4; ++c) {
+          const int hf = c >> 1, h = c & 1;
+          float x[32];
+          uint32_t y[16], z[kTwoTerms ? 16 : 1];
+          tmem_ld32(sc + 32 * c, x);
+          tmem_wait_ld();
+          regs_after_wait(x);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = 2 * hf + h;
-            float x[32];
-            uint32_t y[16];
-            tmem_ld32(sc + 32 * c, x);
-            tmem_wait_ld();
-            regs_after_wait(x);
-            const uint32_t b = hf ? sees[2 + h] : sees[h];
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 k = kscale[8 * c + e / 4], v = vscale[8 * c + e / 4];
-              const float ks[4] = {k.x, k.y, k.z, k.w}, vs[4] = {v.x, v.y, v.z, v.w};
-              float wt[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float pw = ex2(fmaf(x[e + i], ks[i], -ref));
-                wt[i] = pw * vs[i];
-                if (!whole && !(b >> (e + i) & 1)) pw = wt[i] = 0.f;   // 0 times whatever an unseen key's scale is
-                sum[i & 1] += pw;
-              }
-#pragma unroll
-              for (int i = 0; i < 4; i += 2) {
-                y[(e + i) / 2] = pack_bf16(wt[i], wt[i + 1]);
-                if constexpr (kTwoTerms) z[h][(e + i) / 2] = pack_rest(wt[i], wt[i + 1], y[(e + i) / 2]);
-              }
-            }
-            tmem_st16(sc + 64 * hf + 16 * h, y);
+          for (int e = 0; e < 32; e += 4) {
+            const float4 k = kscale[8 * c + e / 4];
+            x[e] = ex2(fmaf(x[e], k.x, -ref)), x[e + 1] = ex2(fmaf(x[e + 1], k.y, -ref));
+            x[e + 2] = ex2(fmaf(x[e + 2], k.z, -ref)), x[e + 3] = ex2(fmaf(x[e + 3], k.w, -ref));
           }
-          // over logits that have all been read by now
+          const uint32_t b = c < 2 ? (c ? sees[1] : sees[0]) : (c == 2 ? sees[2] : sees[3]);
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = b >> e & 1 ? x[e] : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 v = vscale[8 * c + e / 4];
+            sum[0] += x[e] + x[e + 1];
+            sum[1] += x[e + 2] + x[e + 3];
+            x[e] *= v.x, x[e + 1] *= v.y, x[e + 2] *= v.z, x[e + 3] *= v.w;
+          }
+          if (!whole) {                                     // 0 times whatever an unseen key's scale is
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = b >> e & 1 ? x[e] : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            y[e / 2] = pack_bf16(x[e], x[e + 1]);
+            if constexpr (kTwoTerms) z[e / 2] = pack_rest(x[e], x[e + 1], y[e / 2]);
+          }
+          tmem_st16(sc + 64 * hf + 16 * h, y);
           if constexpr (kTwoTerms) {
-            tmem_st16(sc + 64 * hf + 32, z[0]);
-            tmem_st16(sc + 64 * hf + 48, z[1]);
+            // over the half's second group of logits, once that has been read
+            if (h) {
+              tmem_st16(sc + 64 * hf + 32, rest);
+              tmem_st16(sc + 64 * hf + 48, z);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) rest[e] = z[e];
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_ready[2 * t + hf]);
+          if (h) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_ready[2 * t + hf]);
+          }
         }
         l += sum[0] + sum[1];
       }
       if (!ok) break;
-      if (!(ok = mbar_wait_warp(&pv_done[t], (uint32_t)((steps - 1) & 1)))) break;
+      if (!(ok = wait_warp(&pv_done[t], (uint32_t)((steps - 1) & 1)))) break;
       tc_fence_after();
+      float f = 1.f, f1 = 0.f;                              // of this stream's sums, of the other's
+      if (join) {
+        if (t == 1) {
+          swap[0] = m;
+          swap[kTile] = l;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(x_ready);
+          ++joined;
+          continue;
+        }
+        if (!(ok = wait_warp(x_ready, (uint32_t)(joined++ & 1)))) break;
+        tc_fence_after();
+        const float m1 = swap[0], l1 = swap[kTile], both = fmaxf(m, m1);
+        f = m == -INFINITY ? 0.f : ex2(m - both);
+        f1 = m1 == -INFINITY ? 0.f : ex2(m1 - both);
+        // a stream that saw nothing has l = 0, or NaN
+        l = (m == -INFINITY ? l : l * f) + (m1 == -INFINITY ? l1 : l1 * f1);
+        m = both;
+      }
       const bool all = p.lo == 0 && p.hi == p.s.tiles;
       if (!all && p.lo > 0 && threadIdx.x == 0) {
         ta.cuts[blockIdx.x] = Cut{p.begin, p.begin + p.s.tiles, p.b, p.h, p.rb, 1};
         kept = 1;
       }
       float* rec = all ? nullptr
-                       : ta.records + ((int64_t)blockIdx.x * 2 + (p.lo > 0 ? 0 : 1)) * (D + 2) * S::rows + t * kTile + r;
+                       : ta.records + ((int64_t)blockIdx.x * 2 + (p.lo > 0 ? 0 : 1)) * (D + 2) * S::rows + rt * kTile + r;
       const int64_t row = ((int64_t)p.b * a.n + tok) * a.Hq + p.h * ta.G + row_head;
       const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
         tmem_ld32(oc + c, o);
-        tmem_wait_ld();
-        regs_after_wait(o);
+        if (join) {
+          float o1[32];
+          tmem_ld32(oc + 128 + c, o1);
+          tmem_wait_ld();
+          regs_after_wait(o);
+          regs_after_wait(o1);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = (f == 0.f ? 0.f : o[e] * f) + (f1 == 0.f ? 0.f : o1[e] * f1);
+        } else {
+          tmem_wait_ld();
+          regs_after_wait(o);
+        }
         if (all) {
           if (live) {
             T* out = static_cast<T*>(a.out) + row * a.d + c;
@@ -548,6 +622,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         rec[(int64_t)(D + 1) * S::rows] = l;
       }
       tc_fence_before();
+      if (join) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x_free);
+      }
     }
     if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
     if (threadIdx.x == 0 && ta.cuts && !kept) ta.cuts[blockIdx.x].partial = 0;
