@@ -333,14 +333,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         for (int i = 0; ok && item(i, it); ++i) {
           auto load = [&](const CUtensorMap* map, int j) -> bool {
             const int s = st % S::stages;
-            if (!wait(&empty[s], (uint32_t)(((st / S::stages) & 1) ^ 1))) return false;
+            if (!mbar_wait(&empty[s], (uint32_t)(((st / S::stages) & 1) ^ 1))) return false;
             mbar_arrive_expect_tx(&full[s], S::tile);
             for (int sl = 0; sl < S::slabs; ++sl)
               tma_load_3d(map, &full[s], ring + s * S::tile + sl * kTile * 128, sl * 64, it.h, it.start + j * kTile);
             ++st;
             return true;
           };
-          if (i > 0 && !wait(q_free, (uint32_t)((i - 1) & 1))) ok = false;
+          if (i > 0 && !mbar_wait(q_free, (uint32_t)((i - 1) & 1))) ok = false;
           if (ok) {
             const int rows = a.G * a.tq;
             mbar_arrive_expect_tx(q_full, (uint32_t)((it.n[1] ? 2 : 1) * S::slabs * rows * 128));
@@ -360,7 +360,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         if (!ok) atomicOr(a.status, kStatusTimeout);
         // no copy may still be in flight when the block ends
         for (int x = st > S::stages ? st - S::stages : 0; x < st; ++x)
-          if (!wait(&full[x % S::stages], (uint32_t)((x / S::stages) & 1))) atomicOr(a.status, kStatusTimeout);
+          if (!mbar_wait(&full[x % S::stages], (uint32_t)((x / S::stages) & 1))) atomicOr(a.status, kStatusTimeout);
       }
     } else if (warp == 9) {
       // ---------------- MMA
@@ -371,10 +371,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       const uint64_t vd = sw128_mnmajor_desc(smem_u32(ring), kTile * 128);
       int st = 0, pv0 = 0, pv1 = 0;                         // ring steps; value products of tiles 0, 1 so far
       bool ok = true;
-      auto wait_full = [&](int x) { return wait_warp(&full[x % S::stages], (uint32_t)((x / S::stages) & 1)); };
+      auto wait_full = [&](int x) { return mbar_wait_warp(&full[x % S::stages], (uint32_t)((x / S::stages) & 1)); };
       // S of tile t from the K tile of ring step x; the buffer's last P must have been consumed
       auto logits = [&](int t, int pv, int x) -> bool {
-        if (pv > 0 && !wait_warp(&pv_done[t], (uint32_t)((pv - 1) & 1))) return false;
+        if (pv > 0 && !mbar_wait_warp(&pv_done[t], (uint32_t)((pv - 1) & 1))) return false;
         tc_fence_after();
         const uint64_t q = qd + t * (S::tile >> 4), k = kd + (uint32_t)(x % S::stages) * (S::tile >> 4);
 #pragma unroll
@@ -391,7 +391,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         for (int ks = 0; ks < kTile / 16; ++ks) {
           // the weights come in two halves
           if (ks % (kTile / 32) == 0) {
-            if (!wait_warp(&p_ready[2 * t + ks / (kTile / 32)], (uint32_t)(pv & 1))) return false;
+            if (!mbar_wait_warp(&p_ready[2 * t + ks / (kTile / 32)], (uint32_t)(pv & 1))) return false;
             tc_fence_after();
           }
           mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + 8 * ks, v + ks * (2048 >> 4), idesc_o,
@@ -401,7 +401,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         return true;
       };
       for (int i = 0; ok && item(i, it); ++i) {
-        ok = wait_warp(q_full, (uint32_t)(i & 1)) && wait_full(st) && (!it.n[0] || logits(0, pv0, st)) &&
+        ok = mbar_wait_warp(q_full, (uint32_t)(i & 1)) && wait_full(st) && (!it.n[0] || logits(0, pv0, st)) &&
              (!it.n[1] || logits(1, pv1, st));
         if (!ok) break;
         commit(&empty[st % S::stages], lead);
@@ -410,7 +410,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         for (int j = 0; j < it.tiles; ++j) {
           const int xv = st + 2 * j + 1, xk = xv + 1;
           // a tile that some row does not see whole has to be looked through first
-          ok = wait_full(xv) && (j < cut || wait_warp(&clean[xv % S::stages], (uint32_t)((xv / S::stages) & 1)));
+          ok = wait_full(xv) && (j < cut || mbar_wait_warp(&clean[xv % S::stages], (uint32_t)((xv / S::stages) & 1)));
           if (!ok) break;
           const bool more = j + 1 < it.tiles;
           if (j < it.n[0] && !(ok = values(0, pv0++, xv, j == 0))) break;
@@ -427,7 +427,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
       // nothing may still run when tensor memory is given back
       commit(done, lead);
-      if (!wait_warp(done, 0) && lane == 0) atomicOr(a.status, kStatusTimeout);
+      if (!mbar_wait_warp(done, 0) && lane == 0) atomicOr(a.status, kStatusTimeout);
     } else {
       // ---------------- V tiles that some row does not see whole
       const int w = warp - 10;
@@ -440,7 +440,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         for (int j = 0; j < it.tiles; ++j) {
           for (int kv = 0; kv < 2; ++kv, ++st) {
             const int s = st % S::stages;
-            if (!(ok = wait_warp(&full[s], (uint32_t)((st / S::stages) & 1)))) break;
+            if (!(ok = mbar_wait_warp(&full[s], (uint32_t)((st / S::stages) & 1)))) break;
             if (kv && j >= cut) {
               // lane = key of a 32-key group: two groups a warp
               uint8_t* vt = ring + s * S::tile;
@@ -500,7 +500,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       const bool live = row_tok < a.tq && pos < it.len;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++steps) {
-        if (!(ok = wait_warp(&s_full[t], (uint32_t)(steps & 1)))) break;
+        if (!(ok = mbar_wait_warp(&s_full[t], (uint32_t)(steps & 1)))) break;
         tc_fence_after();
         float x[4][32];
 #pragma unroll
@@ -584,7 +584,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         l += s0 + s1;
       }
       if (!ok) break;
-      if (!(ok = wait_warp(&pv_done[t], (uint32_t)((steps - 1) & 1)))) break;
+      if (!(ok = mbar_wait_warp(&pv_done[t], (uint32_t)((steps - 1) & 1)))) break;
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t row = (int64_t)(it.start + pos) * a.Hq + it.h * a.G + row_head;
