@@ -329,23 +329,22 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       // ---------------- converters
       const int w = warp - 12;
       constexpr int kPer = D / 16;                          // 16-byte pieces of a key's codes
-      constexpr int kKeysPerWarp = 32 / kPer;
-      const int u = lane % kPer, sub = lane / kPer;
+      const int key8 = lane & 7, u = lane >> 3;             // eight neighbouring keys, one of four pieces
+      // a piece in the raw row's swizzle (128 or 64 bytes), its two halves in the operand's
+      const uint32_t raw_at = (uint32_t)(key8 * D + ((D == 128 ? u ^ key8 : u ^ (key8 >> 1)) << 4));
       int x = 0, kt = 0;
       bool ok = true;
       auto convert = [&](const uint8_t* raw, uint8_t* dst, auto type) {
+        // 16 keys a warp: their D / 16 pieces in steps of four (lanes / 8) pieces of 8 keys
 #pragma unroll 2
-        for (int k0 = w * kKeysPerWarp; k0 < kTile; k0 += kConverters * kKeysPerWarp) {
-          const int key = k0 + sub;
-          const uint4 c = *reinterpret_cast<const uint4*>(raw + key * D + u * 16);
+        for (int i = 0; i < 2 * kPer / 4; ++i) {
+          const int group = w * 16 + (i & 1) * 8, q = i >> 1;   // eight keys; the four pieces 4 q ..
+          const uint4 c = *reinterpret_cast<const uint4*>(raw + group * D + (raw_at ^ (q << 6)));
           const uint2 e0 = codes4(c.x, type), e1 = codes4(c.y, type), e2 = codes4(c.z, type), e3 = codes4(c.w, type);
-          // 64 coordinates a slab, the second half of a row in the other slab: its
-          // lanes store their two chunks in the other order, off the first's banks
-          uint8_t* rowp = dst + (u >> 2) * kTile * 128 + key * 128;
-          const int c0 = 2 * (u & 3), flip = u >> 2;
-          const uint4 lo = make_uint4(e0.x, e0.y, e1.x, e1.y), hi = make_uint4(e2.x, e2.y, e3.x, e3.y);
-          *reinterpret_cast<uint4*>(rowp + (((c0 + flip) ^ (key & 7)) << 4)) = flip ? hi : lo;
-          *reinterpret_cast<uint4*>(rowp + (((c0 + (flip ^ 1)) ^ (key & 7)) << 4)) = flip ? lo : hi;
+          // 64 coordinates a slab: pieces 4 q .. 4 q + 3 are slab q
+          uint8_t* rowp = dst + q * kTile * 128 + (group + key8) * 128;
+          *reinterpret_cast<uint4*>(rowp + (((2 * u) ^ key8) << 4)) = make_uint4(e0.x, e0.y, e1.x, e1.y);
+          *reinterpret_cast<uint4*>(rowp + (((2 * u + 1) ^ key8) << 4)) = make_uint4(e2.x, e2.y, e3.x, e3.y);
         }
       };
       while (ok && walk.next(a, block_rows, p)) {
@@ -412,8 +411,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         if (!(ok = wait_warp(&s_full[t], (uint32_t)(steps & 1)))) break;
         tc_fence_after();
         const int slot = (base + tile) & 3;
-        const float4* kscale = reinterpret_cast<const float4*>(smem + S::off_sc + slot * S::scales);
-        const float4* vscale = kscale + kTile / 4;
+        const ulonglong2* kscale = reinterpret_cast<const ulonglong2*>(smem + S::off_sc + slot * S::scales);
+        const ulonglong2* vscale = kscale + kTile / 4;
         const int t0 = tile * kTile;
         // which keys the row sees: those that are there, and of the drafted ones its own
         uint32_t sees[4];
@@ -453,8 +452,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           regs_after_wait(x);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 k = kscale[8 * c + e / 4];
-            x[e] *= k.x, x[e + 1] *= k.y, x[e + 2] *= k.z, x[e + 3] *= k.w;
+            const ulonglong2 k = kscale[8 * c + e / 4];
+            unpair(mul2(pair(x[e], x[e + 1]), k.x), x[e], x[e + 1]);
+            unpair(mul2(pair(x[e + 2], x[e + 3]), k.y), x[e + 2], x[e + 3]);
           }
           if (!whole) {
             const uint32_t b = c < 2 ? (c ? sees[1] : sees[0]) : (c == 2 ? sees[2] : sees[3]);
@@ -496,7 +496,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float sum[2] = {0.f, 0.f};
+        const uint64_t ref2 = pair(-ref, -ref);
+        uint64_t sum[2] = {0, 0};
         uint32_t rest[kTwoTerms ? 16 : 1];                  // remainders of the first group of a half
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -508,10 +509,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           regs_after_wait(x);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 k = kscale[8 * c + e / 4];
-            x[e] = ex2(fmaf(x[e], k.x, -ref)), x[e + 1] = ex2(fmaf(x[e + 1], k.y, -ref));
-            x[e + 2] = ex2(fmaf(x[e + 2], k.z, -ref)), x[e + 3] = ex2(fmaf(x[e + 3], k.w, -ref));
+            const ulonglong2 k = kscale[8 * c + e / 4];
+            unpair(fma2(pair(x[e], x[e + 1]), k.x, ref2), x[e], x[e + 1]);
+            unpair(fma2(pair(x[e + 2], x[e + 3]), k.y, ref2), x[e + 2], x[e + 3]);
           }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = ex2(x[e]);
           const uint32_t b = c < 2 ? (c ? sees[1] : sees[0]) : (c == 2 ? sees[2] : sees[3]);
           if (!whole) {
 #pragma unroll
@@ -519,10 +522,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 v = vscale[8 * c + e / 4];
-            sum[0] += x[e] + x[e + 1];
-            sum[1] += x[e + 2] + x[e + 3];
-            x[e] *= v.x, x[e + 1] *= v.y, x[e + 2] *= v.z, x[e + 3] *= v.w;
+            const ulonglong2 v = vscale[8 * c + e / 4];
+            const uint64_t p0 = pair(x[e], x[e + 1]), p1 = pair(x[e + 2], x[e + 3]);
+            sum[0] = add2(sum[0], p0);
+            sum[1] = add2(sum[1], p1);
+            unpair(mul2(p0, v.x), x[e], x[e + 1]);
+            unpair(mul2(p1, v.y), x[e + 2], x[e + 3]);
           }
           if (!whole) {                                     // 0 times whatever an unseen key's scale is
 #pragma unroll
@@ -550,7 +555,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             if (lane == 0) mbar_arrive(&p_ready[2 * t + hf]);
           }
         }
-        l += sum[0] + sum[1];
+        float s0, s1;
+        unpair(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
       }
       if (!ok) break;
       if (!(ok = wait_warp(&pv_done[t], (uint32_t)((steps - 1) & 1)))) break;
@@ -693,7 +700,7 @@ __global__ void __launch_bounds__(NT * kTile) tree_tc_merge_kernel(const TcArgs 
   if (a.lse && blockIdx.y == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// raw rows of one page piece, unswizzled
+// raw rows of one page piece, swizzled so that eight keys' same 16 bytes lie in different banks
 bool raw_map(CUtensorMap* m, const int8_t* base, int d, int64_t rows, int box) {
   const EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return false;
@@ -702,7 +709,7 @@ bool raw_map(CUtensorMap* m, const int8_t* base, int d, int64_t rows, int box) {
   cuuint32_t boxd[2] = {(cuuint32_t)(d <= 64 ? 64 : 128), (cuuint32_t)box};
   cuuint32_t es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides, boxd, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, d <= 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
