@@ -14,16 +14,13 @@
 // softmax runs beside the other's products.  With two row tiles they are the two
 // streams.
 //
-// Warps (640 threads, one block per SM, persistent over equal ranges of 128-key
+// Warps (512 threads, one block per SM, persistent over equal ranges of 128-key
 // tiles; what a cut divides is joined by tree_tc_merge_kernel):
-//   0-3, 4-7  softmax of stream 0, 1: thread = row (TMEM lane); a
-//             tile's logits are read twice, 32 keys at a time (maximum; weights),
-//             in loops that stay small: unrolled over the 128 keys they miss the
-//             instruction cache (7000 cycles a tile)
+//   0-3, 4-7  softmax of stream 0, 1: thread = row (TMEM lane)
 //   8         TMA of the item's queries and of raw code tiles, a page piece at a
 //             time, K and V alternating in a ring
 //   9         the MMA issuer
-//   12-19     converters: raw codes -> swizzled 16-bit operand tiles (one K tile,
+//   12-15     converters: raw codes -> swizzled 16-bit operand tiles (one K tile,
 //             two V tiles), scales and the bits of the keys that are there
 // Tensor memory: S/P of streams 0, 1 at 0, 128; O at 256, 384.  The weights of the
 // first 64 keys take 32 columns from the start of their tile's S, those of the
@@ -45,9 +42,9 @@ using namespace attn;
 using namespace tree;
 
 constexpr int kTile = 128;                    // rows of a row tile, keys of a tile
-constexpr int kThreads = 640;
-constexpr int kConverters = 8;
-constexpr int kRegsSoftmax = 128, kRegsOther = 72;   // 2 x 128 + 3 x 72 <= 5 x 96, the registers at launch
+constexpr int kThreads = 512;
+constexpr int kConverters = 4;
+constexpr int kRegsSoftmax = 192, kRegsOther = 64;   // 2 x 192 + 2 x 64 = 4 x 128, the registers at launch
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr int kBarBytes = 640;   // barriers, valid bits, scratch, the tensor-memory address
 
@@ -56,15 +53,15 @@ struct Shape {
   static constexpr int slabs = D / 64;
   static constexpr int tile = kTile * D * 2;  // bytes of a 16-bit operand tile
   static constexpr int raw = kTile * D;       // bytes of a raw tile
-  static constexpr int scales = 2 * kTile * 4;   // K's and V's, with a K tile
+  static constexpr int scales = 2 * kTile * 4;   // a tile's K and V scales
   static constexpr int stages = D == 128 ? (NT == 2 ? 3 : 5) : 8;
   static constexpr int off_k = NT * tile;
   static constexpr int off_v = off_k + tile;
   static constexpr int off_raw = off_v + 2 * tile;
-  static constexpr int off_rs = off_raw + stages * raw;          // [stages][scales]
-  static constexpr int off_sc = off_rs + stages * scales;        // [4 tiles in turn][K scales x logit scale, V scales][128]
-  static constexpr int off_valid = off_sc + 4 * scales;          // [4][4] words
-  static constexpr int off_swap = off_valid + 4 * 16;            // [2][128] maxima and sums of the second stream
+  static constexpr int off_rows = off_raw + stages * raw;        // [stages][16] cache rows of a K tile's page pieces
+  static constexpr int off_sc = off_rows + stages * 64;          // [4 tiles in turn][K scales x logit scale, V scales][128]
+  static constexpr int off_valid = off_sc + 4 * scales;          // [4][bits of the keys, whether a value scale is not finite][4] words
+  static constexpr int off_swap = off_valid + 4 * 32;            // [2][128] maxima and sums of the second stream
   static constexpr int off_bar = off_swap + 2 * kTile * 4;
   static constexpr int bytes = off_bar + kBarBytes + 1024;
   static constexpr int rows = NT * kTile;
@@ -129,9 +126,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   uint64_t* x_ready = pv_done + 2;              // 4 warps of stream 1: its maxima and sums written, its values done
   uint64_t* x_free = x_ready + 1;               // 4 warps of stream 0: they and its O read
   uint64_t* done = x_free + 1;
-  int64_t* scratch = reinterpret_cast<int64_t*>(done + 1);                // [2 + 20]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 22);
-  static_assert((4 * S::stages + 19 + 22) * 8 + 4 <= kBarBytes && S::bytes <= 232448, "shared memory");
+  int64_t* scratch = reinterpret_cast<int64_t*>(done + 1);                // [2 + 16]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 18);
+  static_assert((4 * S::stages + 19 + 18) * 8 + 4 <= kBarBytes && S::bytes <= 232448, "shared memory");
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::stages; ++s) {
@@ -212,6 +209,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
               ok = false;
               break;
             }
+            if (kv == 0 && lane < 16) reinterpret_cast<int*>(smem + S::off_rows)[s * 16 + lane] = row;
+            __syncwarp();
             if (lane == 0) {
               if (kv == 0) {
                 const int left = p.s.T - tile * kTile;
@@ -226,16 +225,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                   valid[2 * s + half] = bits;
                 }
               }
-              mbar_arrive_expect_tx(&raw_full[s], (uint32_t)(__popc(live) * ta.box * (D + (kv ? 0 : 8))));
+              mbar_arrive_expect_tx(&raw_full[s], (uint32_t)(__popc(live) * ta.box * D));
             }
             __syncwarp();
             if (row >= 0) {
               tma_load_2d(kv ? &vmap : &kmap, &raw_full[s], smem + S::off_raw + s * S::raw + lane * ta.box * D, 0, row);
-              if (kv == 0) {
-                uint8_t* sc = smem + S::off_rs + s * S::scales + lane * ta.box * 4;
-                bulk_load(sc, a.kscales + row, ta.box * 4, &raw_full[s]);
-                bulk_load(sc + kTile * 4, a.vscales + row, ta.box * 4, &raw_full[s]);
-              }
             }
           }
           row = next;
@@ -335,16 +329,22 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       int x = 0, kt = 0;
       bool ok = true;
       auto convert = [&](const uint8_t* raw, uint8_t* dst, auto type) {
-        // 16 keys a warp: their D / 16 pieces in steps of four (lanes / 8) pieces of 8 keys
-#pragma unroll 2
-        for (int i = 0; i < 2 * kPer / 4; ++i) {
-          const int group = w * 16 + (i & 1) * 8, q = i >> 1;   // eight keys; the four pieces 4 q ..
-          const uint4 c = *reinterpret_cast<const uint4*>(raw + group * D + (raw_at ^ (q << 6)));
-          const uint2 e0 = codes4(c.x, type), e1 = codes4(c.y, type), e2 = codes4(c.z, type), e3 = codes4(c.w, type);
-          // 64 coordinates a slab: pieces 4 q .. 4 q + 3 are slab q
-          uint8_t* rowp = dst + q * kTile * 128 + (group + key8) * 128;
-          *reinterpret_cast<uint4*>(rowp + (((2 * u) ^ key8) << 4)) = make_uint4(e0.x, e0.y, e1.x, e1.y);
-          *reinterpret_cast<uint4*>(rowp + (((2 * u + 1) ^ key8) << 4)) = make_uint4(e2.x, e2.y, e3.x, e3.y);
+        // 16 keys of a warp at a time: their D / 16 pieces in steps of four (lanes / 8) pieces of 8 keys
+#pragma unroll 1
+        for (int k0 = w * 16; k0 < kTile; k0 += kConverters * 16) {
+          uint4 c[2 * kPer / 4];
+#pragma unroll
+          for (int i = 0; i < 2 * kPer / 4; ++i)
+            c[i] = *reinterpret_cast<const uint4*>(raw + (k0 + (i & 1) * 8) * D + (raw_at ^ ((i >> 1) << 6)));
+#pragma unroll
+          for (int i = 0; i < 2 * kPer / 4; ++i) {
+            const int group = k0 + (i & 1) * 8, q = i >> 1;   // eight keys; the four pieces 4 q ..
+            const uint2 e0 = codes4(c[i].x, type), e1 = codes4(c[i].y, type), e2 = codes4(c[i].z, type), e3 = codes4(c[i].w, type);
+            // 64 coordinates a slab: pieces 4 q .. 4 q + 3 are slab q
+            uint8_t* rowp = dst + q * kTile * 128 + (group + key8) * 128;
+            *reinterpret_cast<uint4*>(rowp + (((2 * u) ^ key8) << 4)) = make_uint4(e0.x, e0.y, e1.x, e1.y);
+            *reinterpret_cast<uint4*>(rowp + (((2 * u + 1) ^ key8) << 4)) = make_uint4(e2.x, e2.y, e3.x, e3.y);
+          }
         }
       };
       while (ok && walk.next(a, block_rows, p)) {
@@ -356,6 +356,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                  (kv ? kt < 2 || wait_warp(&v_free[buf], (uint32_t)(((kt >> 1) - 1) & 1))
                      : kt < 1 || wait_warp(k_free, (uint32_t)((kt - 1) & 1)));
             if (!ok) break;
+            // the scales of this warp's keys, on their way while the codes are converted
+            const int key = w * 32 + lane;
+            const bool there = !kv && (valid[2 * s + (key >> 6)] >> (key & 63) & 1);
+            float ksc = 0.f, vsc = 0.f;
+            if (there) {
+              const int64_t at = reinterpret_cast<const int*>(smem + S::off_rows)[s * 16 + key / ta.box] + key % ta.box;
+              ksc = __ldg(a.kscales + at);
+              vsc = __ldg(a.vscales + at);
+            }
             uint8_t* dst = smem + (kv ? S::off_v + buf * S::tile : S::off_k);
             if constexpr (kTwoTerms) {
               if (kv) convert(raw, dst, __nv_bfloat16());
@@ -364,15 +373,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
               convert(raw, dst, T());
             }
             if (kv == 0) {
-              if (w < 4) {
-                const int key = w * 32 + lane;
-                const float* rs = reinterpret_cast<const float*>(smem + S::off_rs + s * S::scales);
-                float* sc = reinterpret_cast<float*>(smem + S::off_sc + (kt & 3) * S::scales);
-                const uint32_t bits = (uint32_t)(valid[2 * s + (w >> 1)] >> (32 * (w & 1)));
-                const bool there = bits >> lane & 1;
-                sc[key] = there ? rs[key] * a.scale_log2 : 0.f;
-                sc[kTile + key] = there ? rs[kTile + key] : 0.f;
-                if (lane == 0) reinterpret_cast<uint32_t*>(smem + S::off_valid)[(kt & 3) * 4 + w] = bits;
+              float* sc = reinterpret_cast<float*>(smem + S::off_sc + (kt & 3) * S::scales);
+              sc[key] = ksc * a.scale_log2;
+              sc[kTile + key] = vsc;
+              const uint32_t bits = __ballot_sync(kFull, there);
+              const bool odd = __any_sync(kFull, !(vsc < INFINITY));
+              if (lane == 0) {
+                uint32_t* to = reinterpret_cast<uint32_t*>(smem + S::off_valid) + (kt & 3) * 8 + w;
+                to[0] = bits;
+                to[4] = odd;
               }
             }
             fence_async_smem();
@@ -410,18 +419,17 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       for (int tile = first; tile < p.hi; tile += by, ++steps) {
         if (!(ok = wait_warp(&s_full[t], (uint32_t)(steps & 1)))) break;
         tc_fence_after();
+        float x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(sc + 32 * c, x[c]);
         const int slot = (base + tile) & 3;
         const ulonglong2* kscale = reinterpret_cast<const ulonglong2*>(smem + S::off_sc + slot * S::scales);
         const ulonglong2* vscale = kscale + kTile / 4;
         const int t0 = tile * kTile;
         // which keys the row sees: those that are there, and of the drafted ones its own
-        uint32_t sees[4];
-        bool whole = t0 + kTile <= p.s.ctx;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          sees[c] = reinterpret_cast<const uint32_t*>(smem + S::off_valid)[slot * 4 + c];
-          whole = whole && sees[c] == kFull;
-        }
+        const uint4 there = *reinterpret_cast<const uint4*>(smem + S::off_valid + slot * 32);
+        uint32_t sees[4] = {there.x, there.y, there.z, there.w};
+        const bool whole = t0 + kTile <= p.s.ctx && (there.x & there.y & there.z & there.w) == kFull;
         if (!whole) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -443,32 +451,33 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             sees[c] &= bits;
           }
         }
-        float top = -INFINITY;
-#pragma unroll 1
+        tmem_wait_ld();
+        // base-2 logits, and the row's largest
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float x[32];
-          tmem_ld32(sc + 32 * c, x);
-          tmem_wait_ld();
-          regs_after_wait(x);
+          regs_after_wait(x[c]);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const ulonglong2 k = kscale[8 * c + e / 4];
-            unpair(mul2(pair(x[e], x[e + 1]), k.x), x[e], x[e + 1]);
-            unpair(mul2(pair(x[e + 2], x[e + 3]), k.y), x[e + 2], x[e + 3]);
+            unpair(mul2(pair(x[c][e], x[c][e + 1]), k.x), x[c][e], x[c][e + 1]);
+            unpair(mul2(pair(x[c][e + 2], x[c][e + 3]), k.y), x[c][e + 2], x[c][e + 3]);
           }
-          if (!whole) {
-            const uint32_t b = c < 2 ? (c ? sees[1] : sees[0]) : (c == 2 ? sees[2] : sees[3]);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = b >> e & 1 ? x[e] : -INFINITY;
-          }
-          float mx[2] = {x[0], x[1]};
-#pragma unroll
-          for (int e = 2; e < 30; e += 4) {
-            mx[0] = max3(mx[0], x[e], x[e + 1]);
-            mx[1] = max3(mx[1], x[e + 2], x[e + 3]);
-          }
-          top = max3(top, max3(mx[0], x[30], x[31]), mx[1]);
         }
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[c][e] = sees[c] >> e & 1 ? x[c][e] : -INFINITY;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = max3(x[c][0], x[c][1], x[c][2]);
+#pragma unroll
+          for (int e = 3; e + 1 < 32; e += 2) mx[c] = max3(mx[c], x[c][e], x[c][e + 1]);
+          mx[c] = max3(mx[c], x[c][31], x[c][31]);
+        }
+        const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
         if (!(top < INFINITY)) l = NAN;                     // a seen logit is NaN or infinite: so is the row
         const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
         if (__any_sync(kFull, grow)) {
@@ -498,62 +507,44 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         const float ref = m == -INFINITY ? 0.f : m;
         const uint64_t ref2 = pair(-ref, -ref);
         uint64_t sum[2] = {0, 0};
-        uint32_t rest[kTwoTerms ? 16 : 1];                  // remainders of the first group of a half
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const int hf = c >> 1, h = c & 1;
-          float x[32];
-          uint32_t y[16], z[kTwoTerms ? 16 : 1];
-          tmem_ld32(sc + 32 * c, x);
-          tmem_wait_ld();
-          regs_after_wait(x);
+        // 0 times a scale that is not finite is NaN; such keys are drafted ones that
+        // someone else sees, or nobody
+        const uint4 odd = *reinterpret_cast<const uint4*>(smem + S::off_valid + slot * 32 + 16);
+        const bool clean = whole || !(odd.x | odd.y | odd.z | odd.w);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const ulonglong2 k = kscale[8 * c + e / 4];
-            unpair(fma2(pair(x[e], x[e + 1]), k.x, ref2), x[e], x[e + 1]);
-            unpair(fma2(pair(x[e + 2], x[e + 3]), k.y, ref2), x[e + 2], x[e + 3]);
-          }
+        for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = ex2(x[e]);
-          const uint32_t b = c < 2 ? (c ? sees[1] : sees[0]) : (c == 2 ? sees[2] : sees[3]);
-          if (!whole) {
+          for (int h = 0; h < 2; ++h) {
+            const int c = 2 * hf + h;
+            uint32_t y[16], z[kTwoTerms ? 16 : 1];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = b >> e & 1 ? x[e] : 0.f;
-          }
+            for (int e = 0; e < 32; e += 4) {
+              const ulonglong2 v = vscale[8 * c + e / 4];
+              float* q = x[c] + e;
+              unpair(add2(pair(q[0], q[1]), ref2), q[0], q[1]);
+              unpair(add2(pair(q[2], q[3]), ref2), q[2], q[3]);
+              const uint64_t p0 = pair(ex2(q[0]), ex2(q[1])), p1 = pair(ex2(q[2]), ex2(q[3]));
+              sum[0] = add2(sum[0], p0);
+              sum[1] = add2(sum[1], p1);
+              unpair(mul2(p0, v.x), q[0], q[1]);
+              unpair(mul2(p1, v.y), q[2], q[3]);
+            }
+            if (!clean) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const ulonglong2 v = vscale[8 * c + e / 4];
-            const uint64_t p0 = pair(x[e], x[e + 1]), p1 = pair(x[e + 2], x[e + 3]);
-            sum[0] = add2(sum[0], p0);
-            sum[1] = add2(sum[1], p1);
-            unpair(mul2(p0, v.x), x[e], x[e + 1]);
-            unpair(mul2(p1, v.y), x[e + 2], x[e + 3]);
-          }
-          if (!whole) {                                     // 0 times whatever an unseen key's scale is
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = b >> e & 1 ? x[e] : 0.f;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            y[e / 2] = pack_bf16(x[e], x[e + 1]);
-            if constexpr (kTwoTerms) z[e / 2] = pack_rest(x[e], x[e + 1], y[e / 2]);
-          }
-          tmem_st16(sc + 64 * hf + 16 * h, y);
-          if constexpr (kTwoTerms) {
-            // over the half's second group of logits, once that has been read
-            if (h) {
-              tmem_st16(sc + 64 * hf + 32, rest);
-              tmem_st16(sc + 64 * hf + 48, z);
+              for (int e = 0; e < 32; ++e) x[c][e] = sees[c] >> e & 1 ? x[c][e] : 0.f;
             }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) rest[e] = z[e];
+            for (int e = 0; e < 32; e += 2) {
+              y[e / 2] = pack_bf16(x[c][e], x[c][e + 1]);
+              if constexpr (kTwoTerms) z[e / 2] = pack_rest(x[c][e], x[c][e + 1], y[e / 2]);
+            }
+            tmem_st16(sc + 64 * hf + 16 * h, y);
+            if constexpr (kTwoTerms) tmem_st16(sc + 64 * hf + 32 + 16 * h, z);
           }
-          if (h) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready[2 * t + hf]);
-          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[2 * t + hf]);
         }
         float s0, s1;
         unpair(add2(sum[0], sum[1]), s0, s1);

@@ -293,7 +293,7 @@ struct TreeArgs {
 size_t tree_workspace(const tq_ctx* h, int B, int n, int Hq, int Hkv);
 int launch_tree(const tq_ctx* h, const TreeArgs& a, int dtype, void* workspace, void* stream);
 // more rows of a kv-head than this take the tcgen05 kernel
-constexpr int kTreeTcRows = 16;
+constexpr int kTreeTcRows = 32;
 bool tree_tc_supported(const tq_ctx* h, int n, int Hq, int Hkv);
 size_t tree_tc_workspace(const tq_ctx* h, int n, int Hq, int Hkv);
 int launch_tree_tc(const tq_ctx* h, const TreeArgs& a, int dtype, void* workspace, void* stream);
