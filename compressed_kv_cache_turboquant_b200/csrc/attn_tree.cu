@@ -27,7 +27,7 @@
 // whatever the lengths are.  An item that a cut divides leaves softmax records
 // in the workspace, at most two a block, which tree_merge_kernel joins.
 //
-// A warp of a second warpgroup keeps a ring of tiles filled: one TMA load per page piece for
+// A warp beside them keeps a ring of tiles filled: one TMA load per page piece for
 // the codes (rows of 64 or 128 bytes, swizzled so that the lanes' 16-byte reads
 // never share a bank), bulk copies for the scales, and a word of valid-key bits.
 #include <cuda_bf16.h>
@@ -48,11 +48,7 @@ using namespace tree;
 
 constexpr int kKeys = 64;            // keys of a tile
 constexpr int kWarps = 4;            // consumer warps, 16 keys of a tile each
-constexpr int kThreads = 2 * kWarps * 32;  // a warpgroup of consumers, one of which a single warp feeds the ring
-constexpr int kBlocksPerSm = 2;
-// registers: 128 a thread at launch; the consumers take what the other
-// warpgroup gives back (216 + 40 = 2 x 128)
-constexpr int kRegsConsumer = 216, kRegsProducer = 40;
+constexpr int kRegsConsumer = 216, kRegsProducer = 40;   // 216 + 40 = 2 x 128, the registers at launch
 
 // what the shared window holds, by padded dimension and rows of a block
 template <int D, int MT>
@@ -63,9 +59,16 @@ struct Shape {
   static constexpr int codes = kKeys * D;
   static constexpr int stage = 2 * codes;                  // K and V codes (the swizzle repeats every 1024 bytes)
   static constexpr int scales = 2 * kKeys * 4;             // their scales
-  static constexpr int stages = D == 256 ? 2 : D == 128 ? 5 : 8;
   static constexpr int ksteps = D / 16;
-  static constexpr bool q_in_regs = MT * ksteps <= 8;
+  // 16 rows of up to 128 coordinates fit 128 registers a thread (with the query
+  // fragments in shared memory): three blocks of five warps on an SM.  Wider ones
+  // take two blocks of two warpgroups, of which the consumers' takes registers
+  // that the other, a single warp of which feeds the ring, gives back.
+  static constexpr bool slim = MT == 1 && D <= 128;
+  static constexpr int blocks_per_sm = slim ? 3 : 2;
+  static constexpr int threads = (slim ? kWarps + 1 : 2 * kWarps) * 32;
+  static constexpr int stages = D == 256 ? 2 : D == 128 ? (slim ? 3 : 5) : (slim ? 6 : 8);
+  static constexpr bool q_in_regs = !slim && MT * ksteps <= 8;
   static constexpr int off_scales = stages * stage;
   static constexpr int off_acc = off_scales + stages * scales;   // [rows][D + 4] merged value sums
   static constexpr int off_q = off_acc + rows * (D + 4) * 4;
@@ -146,7 +149,7 @@ template <>
 __device__ __forceinline__ uint32_t q_pair<__half>(uint32_t w, float) { return w; }
 
 template <int D, int MT, typename T>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(Shape<D, MT>::threads, Shape<D, MT>::blocks_per_sm)
 tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, TreeArgs a, int box,
             float* records, Cut* cuts) {
   using S = Shape<D, MT>;
@@ -167,7 +170,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     fence_mbar_init();
   }
   Walk<kKeys> walk;
-  if (!range_of_block<kKeys, kThreads>(a, S::rows, found, walk)) {
+  if (!range_of_block<kKeys, S::threads>(a, S::rows, found, walk)) {
     if (threadIdx.x == 0 && cuts) cuts[blockIdx.x].partial = 0;
     return;
   }
@@ -175,7 +178,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 
   if (warp >= kWarps) {
     // ---------------- producer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
+    if constexpr (!S::slim) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
     if (warp > kWarps) return;
     const int64_t pages = a.rows / a.page;
     const int boxes = kKeys / box;
@@ -239,7 +242,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
   }
 
   // ---------------- consumers
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsumer));
+  if constexpr (!S::slim) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsumer));
   const int g = lane >> 2, c = lane & 3;
   const int G = a.Hq / a.Hkv;
   const uint32_t ring = smem_u32(smem);
@@ -384,8 +387,6 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
         const float ksc[4] = {k0.x, k0.y, k1.x, k1.y};
         const bool masked = there != 0xFFFFu || t0 + 16 > p.s.ctx;
         uint32_t seen[MT][2];                                // bit nt * 2 + e: the row sees that key
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) seen[mt][0] = seen[mt][1] = 0xFu;
         if (masked) {
           uint32_t any = 0;
 #pragma unroll
@@ -410,18 +411,32 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
             }
         }
         // base-2 logits, and whether one passes its row's reference by too much
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint64_t f2 = pair(rowf[mt][hf], rowf[mt][hf]);
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              float* z = sc[mt][nt] + 2 * hf;
+              unpair(mul2(pair(z[0], z[1]), mul2(pair(ksc[2 * nt], ksc[2 * nt + 1]), f2)), z[0], z[1]);
+            }
+          }
+        if (masked) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+                if (!(seen[mt][hf] >> x & 1)) sc[mt][x >> 1][2 * hf + (x & 1)] = -INFINITY;
+        }
         bool grow = false;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              float& z = sc[mt][x >> 1][2 * hf + (x & 1)];
-              z *= ksc[x] * rowf[mt][hf];
-              if (masked && !(seen[mt][hf] >> x & 1)) z = -INFINITY;
-              grow |= z > thr[mt][hf];
-            }
+          for (int hf = 0; hf < 2; ++hf)
+            grow |= fmaxf(fmaxf(sc[mt][0][2 * hf], sc[mt][0][2 * hf + 1]), fmaxf(sc[mt][1][2 * hf], sc[mt][1][2 * hf + 1])) > thr[mt][hf];
         if (__any_sync(kFull, grow)) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
@@ -451,16 +466,30 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              const float x = ex2(sc[mt][nt][2 * hf] - ref[mt][hf]), y = ex2(sc[mt][nt][2 * hf + 1] - ref[mt][hf]);
+              float* z = sc[mt][nt] + 2 * hf;
+              const float x = ex2(z[0] - ref[mt][hf]), y = ex2(z[1] - ref[mt][hf]);
               l[mt][hf] += x + y;
-              float wx = x * vsc[2 * nt], wy = y * vsc[2 * nt + 1];
-              if (masked) {                                  // 0 times whatever an unseen key's scale is
-                if (!(seen[mt][hf] >> (2 * nt) & 1)) wx = 0.f;
-                if (!(seen[mt][hf] >> (2 * nt + 1) & 1)) wy = 0.f;
-              }
-              const uint32_t w = pack_bf16(wx, wy);
+              z[0] = x * vsc[2 * nt], z[1] = y * vsc[2 * nt + 1];
+            }
+        if (masked) {                                        // 0 times whatever an unseen key's scale is
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+                if (!(seen[mt][hf] >> x & 1)) sc[mt][x >> 1][2 * hf + (x & 1)] = 0.f;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const float* z = sc[mt][nt] + 2 * hf;
+              const uint32_t w = pack_bf16(z[0], z[1]);
               pa[mt][2 * nt + hf] = w;
-              if constexpr (kTwoTerms) pr[mt][2 * nt + hf] = pack_rest(wx, wy, w);
+              if constexpr (kTwoTerms) pr[mt][2 * nt + hf] = pack_rest(z[0], z[1], w);
             }
         // O += P C': lane's keys 2c, 2c + 1, 2c + 8, 2c + 9, coordinates g * D/8 ..
 #pragma unroll
@@ -656,20 +685,22 @@ template <int D, int MT, typename T>
 int launch_shape(const TreeArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int box, int grid, bool merge,
                  void* workspace, cudaStream_t st) {
   using S = Shape<D, MT>;
-  static_assert(S::bytes <= 113 * 1024, "two blocks must fit on an SM");
+  static_assert(S::bytes + 1024 <= 228 * 1024 / S::blocks_per_sm, "the blocks of an SM must fit");
   int e = ensure_dyn_smem(reinterpret_cast<const void*>(tree_kernel<D, MT, T>), S::bytes);
   if (e) return e;
   Cut* cuts = static_cast<Cut*>(workspace);
   float* records = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((size_t)grid * sizeof(Cut) + 255) / 256 * 256);
-  tree_kernel<D, MT, T><<<grid, kThreads, S::bytes, st>>>(km, vm, a, box, merge ? records : nullptr, merge ? cuts : nullptr);
+  tree_kernel<D, MT, T><<<grid, S::threads, S::bytes, st>>>(km, vm, a, box, merge ? records : nullptr, merge ? cuts : nullptr);
   e = (int)cudaGetLastError();
   if (e || !merge) return e;
   tree_merge_kernel<D, MT, T><<<grid - 1, 128, 0, st>>>(a, grid, records, cuts);
   return (int)cudaGetLastError();
 }
 
-int tree_grid(const tq_ctx* h, int B, int Hkv, int64_t row_blocks, int64_t tiles) {
-  const int64_t most = (int64_t)h->sm_count * kBlocksPerSm;
+int blocks_per_sm(int d, int mt) { return mt == 1 && d <= 128 ? 3 : 2; }
+
+int tree_grid(const tq_ctx* h, int blocks_sm, int B, int Hkv, int64_t row_blocks, int64_t tiles) {
+  const int64_t most = (int64_t)h->sm_count * blocks_sm;
   const int64_t items = (int64_t)B * Hkv * row_blocks;
   // compare without the product's overflow
   return (int)(items >= most || tiles >= most ? most : std::min(most, items * tiles));
@@ -681,7 +712,7 @@ size_t tree_workspace(const tq_ctx* h, int B, int n, int Hq, int Hkv) {
   if (B == 0 || n == 0 || Hq == 0) return 0;
   if (tree_tc_supported(h, n, Hq, Hkv)) return tree_tc_workspace(h, n, Hq, Hkv);
   const int64_t rows = (int64_t)n * (Hq / Hkv);
-  const int mt = row_tiles(h->d, rows), grid = h->sm_count * kBlocksPerSm;
+  const int mt = row_tiles(h->d, rows), grid = h->sm_count * blocks_per_sm(h->d, mt);
   return ((size_t)grid * sizeof(Cut) + 255) / 256 * 256 + (size_t)grid * 2 * 16 * mt * (padded(h->d) + 2) * 4;
 }
 
@@ -697,8 +728,9 @@ int launch_tree(const tq_ctx* h, const TreeArgs& a, int dtype, void* workspace, 
   const int64_t blocks = (rows + 16 * mt - 1) / (16 * mt), tiles = ((int64_t)a.max_pages * a.page + kKeys - 1) / kKeys;
   const int64_t items = a.B * (int64_t)a.Hkv * blocks;
   const bool merge = tiles > 1;
-  int grid = tree_grid(h, a.B, a.Hkv, blocks, tiles);
-  if (!merge) grid = (int)std::min<int64_t>(items, (int64_t)h->sm_count * kBlocksPerSm);
+  const int per_sm = blocks_per_sm(h->d, mt);
+  int grid = tree_grid(h, per_sm, a.B, a.Hkv, blocks, tiles);
+  if (!merge) grid = (int)std::min<int64_t>(items, (int64_t)h->sm_count * per_sm);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == TQ_BF16;
 #define TQ_TREE(D, MT)                                                                                      \
