@@ -325,50 +325,69 @@ def _dtype3(t: torch.Tensor) -> int:
         raise ValueError(f"unsupported dtype {t.dtype}") from None
 
 
+# These calls are made for every layer of every step, so their checks are written
+# to cost little: device numbers instead of device objects, sizes instead of shapes.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream_on(stream, t: torch.Tensor) -> int:
     """The given stream, or the current one of the device that holds t."""
     if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
+        return _raw_stream(t.get_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _same_device(*tensors) -> None:
-    dev = None
+def _same_device(first: torch.Tensor, *rest) -> None:
+    try:
+        dev = first.get_device()
+        if dev < 0:
+            raise ValueError("expected a CUDA tensor (this library has no CPU path)")
+        for t in rest:
+            if t is not None and t.get_device() != dev:
+                raise ValueError("expected a CUDA tensor (this library has no CPU path)" if t.get_device() < 0 else
+                                 f"tensors on {first.device} and {t.device}")
+    except AttributeError:
+        raise TypeError("expected a torch.Tensor") from None
+
+
+def _dense(*tensors) -> list:
+    """The addresses of contiguous tensors (None for None)."""
+    out = []
     for t in tensors:
         if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("expected a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor (this library has no CPU path)")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
+            out.append(None)
+        elif t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            raise ValueError("expected a contiguous tensor")
+    return out
 
 
 def _token_rows(t: torch.Tensor, name: str, heads: int, d: int) -> int:
     """Checks [tokens][heads][d] with whole heads side by side; returns the
     elements from one token to the next (a slice of a fused projection has more
     than heads d of them)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+    if t.dim() != 3 or t.size(1) != heads or t.size(2) != d:
         raise ValueError(f"{name}: expected [tokens][{heads}][{d}], got {tuple(t.shape)}")
-    if t.numel() and ((d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d)):
+    if t.is_contiguous():
+        return heads * d
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
         raise ValueError(f"{name}: the heads of a token must lie side by side")
-    return t.stride(0) if t.shape[0] > 1 else heads * d
+    return t.stride(0) if t.size(0) > 1 else heads * d
 
 
 def _cache_rows(h: Handle, kcodes, kscales, vcodes, vscales) -> int:
-    """Checks the four cache arrays (the values may be None); returns their rows."""
-    pairs = [(kcodes, kscales)]
-    if vcodes is not None or vscales is not None:
-        pairs.append((vcodes, vscales))
-    for codes, scales in pairs:
-        if codes is None or codes.dtype != torch.int8 or codes.dim() != 2 or codes.shape != (kcodes.shape[0], h.d):
-            raise ValueError(f"codes: expected int8 [rows][{h.d}], the same rows for keys and values")
-        if scales is None or scales.dtype != torch.float32 or scales.shape != kcodes.shape[:1]:
+    """Checks the four cache arrays (the values' may be None); returns their rows."""
+    rows, d = kcodes.size(0), h.d
+    for codes, scales in ((kcodes, kscales), (vcodes, vscales)):
+        if codes is None and scales is None and codes is not kcodes:
+            continue
+        if codes is None or codes.dtype is not torch.int8 or codes.dim() != 2 or codes.size(0) != rows or codes.size(1) != d:
+            raise ValueError(f"codes: expected int8 [rows][{d}], the same rows for keys and values")
+        if scales is None or scales.dtype is not torch.float32 or scales.dim() != 1 or scales.size(0) != rows:
             raise ValueError("scales: expected float32 [rows], as many as the codes")
-    return kcodes.shape[0]
+    return rows
 
 
 def tq_create_kv8(d: int) -> Handle:
@@ -386,19 +405,19 @@ def tq_quant_kv8(h: Handle, k: torch.Tensor, v, slots: torch.Tensor, kcodes: tor
     _same_device(k, v, slots, kcodes, kscales, vcodes, vscales)
     if k.dim() != 3:
         raise ValueError(f"k: expected [tokens][heads][d], got {tuple(k.shape)}")
-    n, Hkv = k.shape[0], k.shape[1]
+    n, Hkv = k.size(0), k.size(1)
     ks = _token_rows(k, "k", Hkv, h.d)
     vs = 0 if v is None else _token_rows(v, "v", Hkv, h.d)
-    if v is not None and (v.shape[0] != n or v.dtype != k.dtype or vcodes is None or vscales is None):
+    if v is not None and (v.size(0) != n or v.dtype != k.dtype or vcodes is None or vscales is None):
         raise ValueError("v: expected as many tokens as k, of its type, and arrays for their codes and scales")
-    if slots.dtype != torch.int64 or slots.numel() != n * Hkv:
+    if slots.dtype is not torch.int64 or slots.numel() != n * Hkv:
         raise ValueError(f"slots: expected int64 [{n}][{Hkv}], got {slots.dtype} {tuple(slots.shape)}")
     rows = _cache_rows(h, kcodes, kscales, vcodes, vscales)
     if n == 0 or Hkv == 0:
         return
     check("tq_quant_kv8", lib.tq_quant_kv8(h.ptr, k.data_ptr(), None if v is None else v.data_ptr(), _dtype3(k), n, Hkv,
-                                           ks, vs, _ptr(slots), _ptr(kcodes), _ptr(kscales), _ptr(vcodes),
-                                           _ptr(vscales), rows, _stream_on(stream, k)))
+                                           ks, vs, *_dense(slots, kcodes, kscales, vcodes, vscales), rows,
+                                           _stream_on(stream, k)))
 
 
 def tq_dequant_kv8(h: Handle, slots: torch.Tensor, kcodes: torch.Tensor, kscales: torch.Tensor, vcodes, vscales,
@@ -406,20 +425,19 @@ def tq_dequant_kv8(h: Handle, slots: torch.Tensor, kcodes: torch.Tensor, kscales
     """Read cache rows slots [n] (int64; outside the cache: zeros) back into k
     and v, [n][d] each (v may be None)."""
     _same_device(slots, kcodes, kscales, vcodes, vscales, k, v)
-    n = slots.numel()
-    if slots.dtype != torch.int64:
+    n, d = slots.numel(), h.d
+    if slots.dtype is not torch.int64:
         raise ValueError(f"slots: expected int64, got {slots.dtype}")
     for t in (k,) if v is None else (k, v):
-        if t.numel() != n * h.d or t.shape[-1] != h.d or t.dtype != k.dtype:
-            raise ValueError(f"outputs: expected [{n}][{h.d}] of one type, got {tuple(t.shape)} {t.dtype}")
+        if t.numel() != n * d or t.size(-1) != d or t.dtype is not k.dtype:
+            raise ValueError(f"outputs: expected [{n}][{d}] of one type, got {tuple(t.shape)} {t.dtype}")
     if v is not None and (vcodes is None or vscales is None):
         raise ValueError("v: needs the values' codes and scales")
     rows = _cache_rows(h, kcodes, kscales, vcodes, vscales)
     if n == 0:
         return
-    check("tq_dequant_kv8", lib.tq_dequant_kv8(h.ptr, n, _ptr(slots), _ptr(kcodes), _ptr(kscales), _ptr(vcodes),
-                                               _ptr(vscales), rows, _ptr(k), _ptr(v), _dtype3(k),
-                                               _stream_on(stream, k)))
+    check("tq_dequant_kv8", lib.tq_dequant_kv8(h.ptr, n, *_dense(slots, kcodes, kscales, vcodes, vscales), rows,
+                                               *_dense(k, v), _dtype3(k), _stream_on(stream, k)))
 
 
 # ---- attention over prompts and over the 8-bit cache
@@ -438,9 +456,9 @@ def _scratch(nbytes: int, like: torch.Tensor, stream):
 
 
 def _outputs(q: torch.Tensor, out: torch.Tensor, lse) -> None:
-    if out.shape != q.shape or out.dtype != q.dtype:
+    if out.shape != q.shape or out.dtype is not q.dtype:
         raise ValueError(f"out: expected {tuple(q.shape)} {q.dtype}, got {tuple(out.shape)} {out.dtype}")
-    if lse is not None and (lse.shape != q.shape[:-1] or lse.dtype != torch.float32):
+    if lse is not None and (lse.shape != q.shape[:-1] or lse.dtype is not torch.float32):
         raise ValueError(f"lse: expected float32 {tuple(q.shape[:-1])}, got {lse.dtype} {tuple(lse.shape)}")
 
 
@@ -468,8 +486,8 @@ def tq_attn_prompt(h: Handle, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if workspace is None:
         workspace = _scratch(tq_attn_prompt_workspace(h, nseq, total, Hq, Hkv), q, stream)
     check("tq_attn_prompt", lib.tq_attn_prompt(
-        h.ptr, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype3(q), _ptr(cu_seqlens), nseq, total, Hq, Hkv, *strides,
-        float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+        h.ptr, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype3(q), *_dense(cu_seqlens), nseq, total, Hq, Hkv, *strides,
+        float(scale), *_dense(out, lse, workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_on(stream, q)))
 
 
@@ -496,7 +514,7 @@ def tq_attn_tree(h: Handle, q: torch.Tensor, Hkv: int, ctx_lens: torch.Tensor, b
         raise ValueError("q: tokens must lie a constant stride apart, their heads side by side")
     for name, t, shape in (("ctx_lens", ctx_lens, (B,)), ("draft_lens", draft_lens, (B,)),
                            ("mask", mask, (B, n, (n + 31) // 32))):
-        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape):
+        if t is not None and (t.dtype is not torch.int32 or t.shape != shape):
             raise ValueError(f"{name}: expected int32 {shape}, got {t.dtype} {tuple(t.shape)}")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B * Hkv:
         raise ValueError(f"block_table: expected int32 [{B * Hkv}][max_pages], got {block_table.dtype} {tuple(block_table.shape)}")
@@ -505,9 +523,9 @@ def tq_attn_tree(h: Handle, q: torch.Tensor, Hkv: int, ctx_lens: torch.Tensor, b
     if workspace is None:
         workspace = _scratch(tq_attn_tree_workspace(h, B, n, Hq, Hkv), q, stream)
     check("tq_attn_tree", lib.tq_attn_tree(
-        h.ptr, q.data_ptr(), _dtype3(q), qs, B, n, Hq, Hkv, _ptr(ctx_lens), _ptr(draft_lens), _ptr(mask),
-        _ptr(block_table), block_table.shape[1], page_size, _ptr(kcodes), _ptr(kscales), _ptr(vcodes), _ptr(vscales),
-        rows, float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+        h.ptr, q.data_ptr(), _dtype3(q), qs, B, n, Hq, Hkv, *_dense(ctx_lens, draft_lens, mask, block_table),
+        block_table.size(1), page_size, *_dense(kcodes, kscales, vcodes, vscales), rows, float(scale),
+        *_dense(out, lse, workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_on(stream, q)))
 
 

@@ -169,9 +169,10 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     }
     fence_mbar_init();
   }
+  asm volatile("griddepcontrol.launch_dependents;");       // the merge may set itself up
   Walk<kKeys> walk;
   if (!range_of_block<kKeys, S::threads>(a, S::rows, found, walk)) {
-    if (threadIdx.x == 0 && cuts) cuts[blockIdx.x].partial = 0;
+    if (threadIdx.x == 0 && cuts) cuts[blockIdx.x].begin = -1;
     return;
   }
   Piece p;
@@ -574,8 +575,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
       // the block's first record is of an item begun elsewhere, its second of one begun here
       rec = records + ((int64_t)blockIdx.x * 2 + (p.lo > 0 ? 0 : 1)) * S::rows * (D + 2);
       if (p.lo > 0 && threadIdx.x == 0) {
-        Cut cut{p.begin, p.begin + p.s.tiles, p.b, p.h, p.rb, 1};
-        cuts[blockIdx.x] = cut;
+        cuts[blockIdx.x] = walk.cut_of(p);
         kept = 1;
       }
     }
@@ -606,51 +606,48 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     }
     named_bar_sync(1, kWarps * 32);                          // acc_sm and ml are free again
   }
-  if (threadIdx.x == 0 && cuts && !kept) cuts[blockIdx.x].partial = 0;
+  if (threadIdx.x == 0 && cuts && !kept) cuts[blockIdx.x].begin = -1;
 }
 
 // Block i > 0: if block i of the main grid began inside an item, and i is the
 // first cut of that item, the records of blocks i - 1 (its second), i, i + 1, ..
-// (their first) become the item's rows.
+// (their first) become the item's rows.  A warp takes a row: first the records'
+// maxima and sums, a lane each, then their value sums one by one.
 template <int D, int MT, typename T>
-__global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, int grid, const float* records, const Cut* cuts) {
+__global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, const float* records, const Cut* cuts) {
   using S = Shape<D, MT>;
+  asm volatile("griddepcontrol.wait;" ::: "memory");         // the main grid is done
   const int i = blockIdx.x + 1;
   const Cut cut = cuts[i];
-  if (!cut.partial) return;
-  __shared__ int64_t total_sm;
-  __shared__ int64_t part[4];
-  int64_t sum = 0;
-  for (int b = threadIdx.x; b < a.B; b += 128) sum += units_of(a, seq_of<kKeys>(a, b, S::rows));
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) total_sm = part[0] + part[1] + part[2] + part[3];
-  __syncthreads();
-  int last;
-  if (!first_cut_of(cut, i, grid, total_sm, last)) return;
+  if (cut.begin != i - 1) return;
+  const int n = cut.end - cut.begin + 1;
   const int G = a.Hq / a.Hkv;
   const int drafts = a.draft_lens ? min(max(__ldg(a.draft_lens + cut.b), 0), a.n) : a.n;
   const int rows = min(S::rows, drafts * G - cut.rb * S::rows);
   const int lane = threadIdx.x & 31;
   for (int r = threadIdx.x >> 5; r < rows; r += 4) {
-    auto rec = [&](int x) { return records + ((int64_t)x * 2 + (x == i - 1 ? 1 : 0)) * S::rows * (D + 2) + r * (D + 2); };
-    float m = -INFINITY;
-    for (int x = i - 1; x <= last; ++x) m = fmaxf(m, rec(x)[D]);
-    float l = 0.f, v[D / 32];
+    auto rec = [&](int x) { return records + ((int64_t)(i - 1 + x) * 2 + (x == 0 ? 1 : 0)) * S::rows * (D + 2) + r * (D + 2); };
+    float m = -INFINITY, l = 0.f;
+    for (int x = lane; x < n; x += 32) m = fmaxf(m, __ldcg(rec(x) + D));
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    for (int x = lane; x < n; x += 32) {
+      const float mx = __ldcg(rec(x) + D), lx = __ldcg(rec(x) + D + 1);
+      l += mx == -INFINITY ? lx : lx * ex2(mx - m);          // nothing seen: 0, or NaN
+    }
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+    float v[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) v[e] = 0.f;
-    for (int x = i - 1; x <= last; ++x) {
+#pragma unroll 4
+    for (int x = 0; x < n; ++x) {
       const float* p = rec(x);
-      const float mx = p[D], lx = p[D + 1];
-      if (mx == -INFINITY) {
-        l += lx;                                             // 0, or NaN
-        continue;
-      }
-      const float f = ex2(mx - m);
-      l += lx * f;
+      const float mx = __ldcg(p + D), f = mx == -INFINITY ? 0.f : ex2(mx - m);
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) v[e] = fmaf(p[lane * 2 + 64 * (e >> 1) + (e & 1)], f, v[e]);
+      for (int e = 0; e < D / 64; ++e) {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(p + 64 * e + 2 * lane));
+        v[2 * e] = f == 0.f ? v[2 * e] : fmaf(y.x, f, v[2 * e]);
+        v[2 * e + 1] = f == 0.f ? v[2 * e + 1] : fmaf(y.y, f, v[2 * e + 1]);
+      }
     }
     const int x = cut.rb * S::rows + r;
     const int64_t row = ((int64_t)cut.b * a.n + x / G) * a.Hq + cut.h * G + x % G;
@@ -693,8 +690,7 @@ int launch_shape(const TreeArgs& a, const CUtensorMap& km, const CUtensorMap& vm
   tree_kernel<D, MT, T><<<grid, S::threads, S::bytes, st>>>(km, vm, a, box, merge ? records : nullptr, merge ? cuts : nullptr);
   e = (int)cudaGetLastError();
   if (e || !merge) return e;
-  tree_merge_kernel<D, MT, T><<<grid - 1, 128, 0, st>>>(a, grid, records, cuts);
-  return (int)cudaGetLastError();
+  return launch_beside(tree_merge_kernel<D, MT, T>, dim3(grid - 1), 128, st, a, (const float*)records, (const Cut*)cuts);
 }
 
 int blocks_per_sm(int d, int mt) { return mt == 1 && d <= 128 ? 3 : 2; }

@@ -12,11 +12,12 @@ namespace tree {
 
 using attn::kFull;
 
-// a block owns two records of the workspace (value sums, maximum and sum of every
-// row); this is the item that its first record belongs to
+// A block owns two records of the workspace (value sums, maximum and sum of every
+// row): the first for an item that began in an earlier block, the second for one
+// that goes on in a later one.  This says which item the first belongs to.
 struct Cut {
-  int64_t begin, end;  // the item's units
-  int b, h, rb, partial;
+  int b, h, rb;
+  int begin, end;  // the blocks that hold the item's first and last unit; begin < 0: no such item
 };
 
 struct Seq {
@@ -50,7 +51,13 @@ struct Piece {
 template <int kKeys>
 struct Walk {
   int64_t u, end, base;
-  int b;
+  int64_t total;
+  int b, blocks;
+  // the block that unit x belongs to: the last whose range begins at or before it
+  __device__ __forceinline__ int block_of(int64_t x) const { return (int)(((x + 1) * blocks - 1) / total); }
+  __device__ __forceinline__ Cut cut_of(const Piece& p) const {
+    return Cut{p.b, p.h, p.rb, block_of(p.begin), block_of(p.begin + p.s.tiles - 1)};
+  }
   __device__ __forceinline__ bool next(const TreeArgs& a, int rows_per_block, Piece& p) {
     if (u >= end) return false;
     p.s = seq_of<kKeys>(a, b, rows_per_block);
@@ -96,6 +103,8 @@ __device__ __forceinline__ bool range_of_block(const TreeArgs& a, int rows, int6
   for (int w = 0; w < kThreads / 32; ++w) total += part[w];
   const int64_t blocks = min((int64_t)gridDim.x, total);
   if (blockIdx.x >= blocks) return false;
+  walk.total = total;
+  walk.blocks = (int)blocks;
   walk.u = total * blockIdx.x / blocks;
   walk.end = total * (blockIdx.x + 1) / blocks;
   if (warp == 0) {
@@ -121,14 +130,20 @@ __device__ __forceinline__ bool range_of_block(const TreeArgs& a, int rows, int6
   return true;
 }
 
-// For block i > 0 of a grid whose block i began inside an item: whether i is that
-// item's first cut, and the last block with a part of it.
-__device__ __forceinline__ bool first_cut_of(const Cut& cut, int i, int grid, int64_t total, int& last) {
-  const int64_t blocks = min((int64_t)grid, total);
-  if (total * (i - 1) / blocks > cut.begin) return false;
-  last = i;
-  while (last + 1 < blocks && total * (last + 1) / blocks < cut.end) ++last;
-  return true;
+// Launches a kernel that may start beside the grid before it (and waits for it by
+// griddepcontrol.wait).
+template <typename... P, typename... A>
+int launch_beside(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace tree

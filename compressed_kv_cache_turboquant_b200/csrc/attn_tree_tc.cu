@@ -154,9 +154,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   }
   // rows of a block in whole tokens: what seq_of counts blocks by
   const int block_rows = NT * ta.tq * ta.G;
+  asm volatile("griddepcontrol.launch_dependents;");       // the merge may set itself up
   Walk<kTile> walk;
   if (!range_of_block<kTile, kThreads>(a, block_rows, scratch, walk)) {
-    if (threadIdx.x == 0 && ta.cuts) ta.cuts[blockIdx.x].partial = 0;
+    if (threadIdx.x == 0 && ta.cuts) ta.cuts[blockIdx.x].begin = -1;
     return;
   }
   if (warp == 9) tmem_alloc(tmem_slot, 512);
@@ -575,7 +576,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       }
       const bool all = p.lo == 0 && p.hi == p.s.tiles;
       if (!all && p.lo > 0 && threadIdx.x == 0) {
-        ta.cuts[blockIdx.x] = Cut{p.begin, p.begin + p.s.tiles, p.b, p.h, p.rb, 1};
+        ta.cuts[blockIdx.x] = walk.cut_of(p);
         kept = 1;
       }
       float* rec = all ? nullptr
@@ -626,7 +627,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       }
     }
     if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
-    if (threadIdx.x == 0 && ta.cuts && !kept) ta.cuts[blockIdx.x].partial = 0;
+    if (threadIdx.x == 0 && ta.cuts && !kept) ta.cuts[blockIdx.x].begin = -1;
   }
   __syncwarp();
   tc_fence_before();
@@ -639,44 +640,36 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 // i is the item's first cut: the second record of block i - 1 and the first ones of
 // i, i + 1, ..  Thread = row; blockIdx.y takes 16 of the coordinates.
 template <int D, int NT, typename T>
-__global__ void __launch_bounds__(NT * kTile) tree_tc_merge_kernel(const TcArgs ta, int grid) {
+__global__ void __launch_bounds__(NT * kTile) tree_tc_merge_kernel(const TcArgs ta) {
   using S = Shape<D, NT>;
   const TreeArgs& a = ta.t;
+  asm volatile("griddepcontrol.wait;" ::: "memory");         // the main grid is done
   const int i = blockIdx.x + 1;
   const Cut cut = ta.cuts[i];
-  if (!cut.partial) return;
-  __shared__ int64_t part[NT * 4];
-  const int block_rows = NT * ta.tq * ta.G;
-  int64_t sum = 0;
-  for (int b = threadIdx.x; b < a.B; b += NT * kTile) sum += units_of(a, seq_of<kTile>(a, b, block_rows));
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < NT * 4; ++w) total += part[w];
-  int last;
-  if (!first_cut_of(cut, i, grid, total, last)) return;
+  if (cut.begin != i - 1) return;
+  const int last = cut.end;
   const int t = threadIdx.x / kTile, row_tok = threadIdx.x % kTile / ta.G, row_head = threadIdx.x % kTile % ta.G;
   const int tok = (cut.rb * NT + t) * ta.tq + row_tok;
   const int drafts = a.draft_lens ? min(max(__ldg(a.draft_lens + cut.b), 0), a.n) : a.n;
   if (row_tok >= ta.tq || tok >= drafts) return;
   auto rec = [&](int x) { return ta.records + ((int64_t)x * 2 + (x == i - 1 ? 1 : 0)) * (D + 2) * S::rows + threadIdx.x; };
   float m = -INFINITY;
-  for (int x = i - 1; x <= last; ++x) m = fmaxf(m, rec(x)[(int64_t)D * S::rows]);
+#pragma unroll 4
+  for (int x = i - 1; x <= last; ++x) m = fmaxf(m, __ldcg(rec(x) + (int64_t)D * S::rows));
   float l = 0.f, v[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e] = 0.f;
+#pragma unroll 2
   for (int x = i - 1; x <= last; ++x) {
     const float* p = rec(x);
-    const float mx = p[(int64_t)D * S::rows], lx = p[(int64_t)(D + 1) * S::rows];
-    if (mx == -INFINITY) {
-      l += lx;                                              // 0, or NaN
-      continue;
-    }
-    const float f = ex2(mx - m);
-    l += lx * f;
+    const float mx = __ldcg(p + (int64_t)D * S::rows), lx = __ldcg(p + (int64_t)(D + 1) * S::rows);
+    const float f = mx == -INFINITY ? 0.f : ex2(mx - m);
+    l += mx == -INFINITY ? lx : lx * f;                     // nothing seen: 0, or NaN
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = fmaf(p[(int64_t)(blockIdx.y * 16 + e) * S::rows], f, v[e]);
+    for (int e = 0; e < 16; ++e) {
+      const float y = __ldcg(p + (int64_t)(blockIdx.y * 16 + e) * S::rows);
+      v[e] = f == 0.f ? v[e] : fmaf(y, f, v[e]);
+    }
   }
   const int64_t row = ((int64_t)cut.b * a.n + tok) * a.Hq + cut.h * ta.G + row_head;
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -717,8 +710,7 @@ int launch_shape(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap
   tree_tc_kernel<D, NT, T><<<grid, kThreads, S::bytes, st>>>(qm, km, vm, ta);
   const int e2 = (int)cudaGetLastError();
   if (e2 || !merge) return e2;
-  tree_tc_merge_kernel<D, NT, T><<<dim3(grid - 1, D / 16), NT * kTile, 0, st>>>(ta, grid);
-  return (int)cudaGetLastError();
+  return launch_beside(tree_tc_merge_kernel<D, NT, T>, dim3(grid - 1, D / 16), NT * kTile, st, ta);
 }
 
 int row_tiles(int64_t rows) { return rows <= kTile ? 1 : 2; }
