@@ -9,12 +9,15 @@
 // scales applied to the float32 logits and to the weights p_t.  Queries enter
 // as fp16 (bf16 ones with a power of two per row: their 8 bits fit; what falls
 // below fp16's range is under 2^-40 of the row's largest), the weights p s' as
-// bf16, whose range holds whatever the scales are.  Their one rounding (2^-9
-// at most) is the size of the result's own in bf16; for fp16 results the
-// remainder of that rounding takes a second product.
+// bf16, whose range holds whatever the scales are, in two terms: rounded once, few
+// keys under a row cost 2^-9 beside the result's own rounding (measured on 1000
+// keys: 0.0028 of the result, 0.0016 with the remainder's product, the plain
+// formula in 64 bits rounded to bf16).  Up to 8 rows the remainders are the other
+// half of the 16-row fragment and cost nothing; for 9 to 32 rows they are a second
+// product (32 sequences of 4000 tokens, 16 rows: 109 us, 103 without).
 //
 // A kv-head's rows (drafted token, head of its group) form the M side of the
-// products, 16 or 32 rows of a block at a time; keys are the N side of the
+// products, 8, 16 or 32 rows of a block at a time; keys are the N side of the
 // logits and the K side of the value product, so a logit fragment becomes a
 // weight fragment in place.  Each of four warps takes 16 of the 64 keys of a
 // tile with its own softmax (maximum, sum, value sum in registers), and the four
@@ -51,9 +54,11 @@ constexpr int kWarps = 4;            // consumer warps, 16 keys of a tile each
 constexpr int kRegsConsumer = 216, kRegsProducer = 40;   // 216 + 40 = 2 x 128, the registers at launch
 
 // what the shared window holds, by padded dimension and rows of a block
-template <int D, int MT>
+template <int D, int R>
 struct Shape {
-  static constexpr int rows = 16 * MT;
+  static constexpr int rows = R;                           // 8, 16 or 32
+  static constexpr int MT = R > 16 ? R / 16 : 1;           // fragments of 16 rows
+  static constexpr int HF = R == 8 ? 1 : 2;                // halves of a fragment that hold rows
   static constexpr int slabs = D > 128 ? D / 128 : 1;      // a row's bytes come in slabs of at most 128
   static constexpr int slab_row = D > 128 ? 128 : D;
   static constexpr int codes = kKeys * D;
@@ -64,7 +69,7 @@ struct Shape {
   // fragments in shared memory): three blocks of five warps on an SM.  Wider ones
   // take two blocks of two warpgroups, of which the consumers' takes registers
   // that the other, a single warp of which feeds the ring, gives back.
-  static constexpr bool slim = MT == 1 && D <= 128;
+  static constexpr bool slim = R <= 16 && D <= 128;
   static constexpr int blocks_per_sm = slim ? 3 : 2;
   static constexpr int threads = (slim ? kWarps + 1 : 2 * kWarps) * 32;
   static constexpr int stages = D == 256 ? 2 : D == 128 ? (slim ? 3 : 5) : (slim ? 6 : 8);
@@ -72,7 +77,7 @@ struct Shape {
   static constexpr int off_scales = stages * stage;
   static constexpr int off_acc = off_scales + stages * scales;   // [rows][D + 4] merged value sums
   static constexpr int off_q = off_acc + rows * (D + 4) * 4;
-  static constexpr int off_ml = off_q + (q_in_regs ? 0 : MT * ksteps * 512);   // [kWarps][rows] maxima, then sums
+  static constexpr int off_ml = off_q + (q_in_regs ? 0 : MT * ksteps * 256 * HF);   // [kWarps][rows] maxima, then sums
   static constexpr int off_bar = off_ml + 2 * kWarps * rows * 4;
   static constexpr int bytes = off_bar + 512 + 1024;
 };
@@ -148,12 +153,13 @@ __device__ __forceinline__ uint32_t q_pair<__nv_bfloat16>(uint32_t w, float f) {
 template <>
 __device__ __forceinline__ uint32_t q_pair<__half>(uint32_t w, float) { return w; }
 
-template <int D, int MT, typename T>
-__global__ void __launch_bounds__(Shape<D, MT>::threads, Shape<D, MT>::blocks_per_sm)
+template <int D, int R, typename T>
+__global__ void __launch_bounds__(Shape<D, R>::threads, Shape<D, R>::blocks_per_sm)
 tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, TreeArgs a, int box,
             float* records, Cut* cuts) {
-  using S = Shape<D, MT>;
-  constexpr bool kTwoTerms = std::is_same<T, __half>::value;
+  using S = Shape<D, R>;
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  constexpr int MT = S::MT, HF = S::HF;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::off_bar);
@@ -257,14 +263,13 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     // queries: fragments of rows (token, head) = divmod(row, G), scaled by a power of two each
     uint32_t qf[S::q_in_regs ? MT : 1][S::q_in_regs ? S::ksteps : 1][4];
     float rowf[MT][2];
-    uint4* qsm = reinterpret_cast<uint4*>(smem + S::off_q);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       constexpr int kChunks = D / 32;                        // 16-byte chunks of a lane's coordinates in a row
-      uint4 raw[2][kChunks];
-      float f[2];
+      uint4 raw[HF][kChunks];
+      float f[HF];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int hf = 0; hf < HF; ++hf) {
         const int r = mt * 16 + hf * 8 + g;
         const bool live = r < live_rows;
         const int x = p.rb * S::rows + r, tok = x / G, hd = x % G;
@@ -276,14 +281,14 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
           // lane c's bytes of a key: D <= 128: c * D/4 ..; above, c * 32 .. of every slab
           const int e = D <= 128 ? c * (D / 4) + 8 * k : (k >> 2) * 128 + c * 32 + 8 * (k & 3);
           raw[hf][k] = live && e < a.d ? __ldg(reinterpret_cast<const uint4*>(q + e)) : make_uint4(0u, 0u, 0u, 0u);
-          if (!kTwoTerms) {
+          if (!kHalf) {
             const uint32_t w[4] = {raw[hf][k].x, raw[hf][k].y, raw[hf][k].z, raw[hf][k].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) mx = max(mx, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
           }
         }
         f[hf] = 1.f;
-        if (!kTwoTerms) {
+        if (!kHalf) {
           mx = max(mx, __shfl_xor_sync(kFull, mx, 1));
           mx = max(mx, __shfl_xor_sync(kFull, mx, 2));
           // the largest of the row at 2^14 .. 2^15; 2^127 at most either way (rows of zeros or subnormals, infinities)
@@ -298,15 +303,20 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
         const uint32_t lo[4] = {raw[0][k].x, raw[0][k].y, raw[0][k].z, raw[0][k].w};
-        const uint32_t hi[4] = {raw[1][k].x, raw[1][k].y, raw[1][k].z, raw[1][k].w};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint32_t a0 = q_pair<T>(lo[2 * j], f[0]), a1 = q_pair<T>(hi[2 * j], f[1]);
-          const uint32_t a2 = q_pair<T>(lo[2 * j + 1], f[0]), a3 = q_pair<T>(hi[2 * j + 1], f[1]);
-          if constexpr (S::q_in_regs) {
-            qf[mt][2 * k + j][0] = a0, qf[mt][2 * k + j][1] = a1, qf[mt][2 * k + j][2] = a2, qf[mt][2 * k + j][3] = a3;
+          const uint32_t a0 = q_pair<T>(lo[2 * j], f[0]), a2 = q_pair<T>(lo[2 * j + 1], f[0]);
+          const int at = (mt * S::ksteps + 2 * k + j) * 32 + lane;
+          if constexpr (HF == 1) {
+            if (warp == mt) reinterpret_cast<uint2*>(smem + S::off_q)[at] = make_uint2(a0, a2);
           } else {
-            if (warp == mt) qsm[(mt * S::ksteps + 2 * k + j) * 32 + lane] = make_uint4(a0, a1, a2, a3);
+            const uint32_t hi[4] = {raw[1][k].x, raw[1][k].y, raw[1][k].z, raw[1][k].w};
+            const uint32_t a1 = q_pair<T>(hi[2 * j], f[1]), a3 = q_pair<T>(hi[2 * j + 1], f[1]);
+            if constexpr (S::q_in_regs) {
+              qf[mt][2 * k + j][0] = a0, qf[mt][2 * k + j][1] = a1, qf[mt][2 * k + j][2] = a2, qf[mt][2 * k + j][3] = a3;
+            } else {
+              if (warp == mt) reinterpret_cast<uint4*>(smem + S::off_q)[at] = make_uint4(a0, a1, a2, a3);
+            }
           }
         }
       }
@@ -322,7 +332,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) thr[mt][hf] = -INFINITY, ref[mt][hf] = 0.f, l[mt][hf] = 0.f;
+      for (int hf = 0; hf < HF; ++hf) thr[mt][hf] = -INFINITY, ref[mt][hf] = 0.f, l[mt][hf] = 0.f;
     }
 
     for (int tile = p.lo; tile < p.hi; ++tile, ++it) {
@@ -373,8 +383,14 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
                   mma_f16(sc[mt][0], qf[mt][ks], b[0][0], b[0][1]);
                   mma_f16(sc[mt][1], qf[mt][ks], b[1][0], b[1][1]);
                 } else {
-                  const uint4 qv = lds128(qbase + ((mt * S::ksteps + ks) * 32 + lane) * 16);
-                  const uint32_t qa[4] = {qv.x, qv.y, qv.z, qv.w};
+                  uint32_t qa[4] = {0u, 0u, 0u, 0u};
+                  if constexpr (HF == 1) {
+                    const uint2 qv = lds64(qbase + ((mt * S::ksteps + ks) * 32 + lane) * 8);
+                    qa[0] = qv.x, qa[2] = qv.y;
+                  } else {
+                    const uint4 qv = lds128(qbase + ((mt * S::ksteps + ks) * 32 + lane) * 16);
+                    qa[0] = qv.x, qa[1] = qv.y, qa[2] = qv.z, qa[3] = qv.w;
+                  }
                   mma_f16(sc[mt][0], qa, b[0][0], b[0][1]);
                   mma_f16(sc[mt][1], qa, b[1][0], b[1][1]);
                 }
@@ -396,7 +412,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
+            for (int hf = 0; hf < HF; ++hf) {
               const int r = mt * 16 + hf * 8 + g;
               const int i = (p.rb * S::rows + r) / G;
               uint32_t bits = any;
@@ -415,7 +431,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
+          for (int hf = 0; hf < HF; ++hf) {
             const uint64_t f2 = pair(rowf[mt][hf], rowf[mt][hf]);
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
@@ -429,20 +445,20 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
+              for (int hf = 0; hf < HF; ++hf)
                 if (!(seen[mt][hf] >> x & 1)) sc[mt][x >> 1][2 * hf + (x & 1)] = -INFINITY;
         }
         bool grow = false;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
+          for (int hf = 0; hf < HF; ++hf)
             grow |= fmaxf(fmaxf(sc[mt][0][2 * hf], sc[mt][0][2 * hf + 1]), fmaxf(sc[mt][1][2 * hf], sc[mt][1][2 * hf + 1])) > thr[mt][hf];
         if (__any_sync(kFull, grow)) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
+            for (int hf = 0; hf < HF; ++hf) {
               float m = fmaxf(fmaxf(sc[mt][0][2 * hf], sc[mt][0][2 * hf + 1]), fmaxf(sc[mt][1][2 * hf], sc[mt][1][2 * hf + 1]));
               m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
               m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
@@ -452,21 +468,20 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
                 thr[mt][hf] = m + kLazy;
                 l[mt][hf] *= f;
 #pragma unroll
-                for (int nt = 0; nt < D / 8; ++nt) {
-                  o[mt][nt][2 * hf] *= f;
-                  o[mt][nt][2 * hf + 1] *= f;
-                }
+                for (int nt = 0; nt < D / 8; ++nt)
+#pragma unroll
+                  for (int e = 2 * hf; e < (HF == 1 ? 4 : 2 * hf + 2); ++e) o[mt][nt][e] *= f;
               }
             }
         }
-        uint32_t pa[MT][4], pr[kTwoTerms ? MT : 1][4];
+        uint32_t pa[MT][4], pr[MT][4];                       // the weights, and what their rounding left
         const float vsc[4] = {v0.x, v0.y, v1.x, v1.y};
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
+            for (int hf = 0; hf < HF; ++hf) {
               float* z = sc[mt][nt] + 2 * hf;
               const float x = ex2(z[0] - ref[mt][hf]), y = ex2(z[1] - ref[mt][hf]);
               l[mt][hf] += x + y;
@@ -478,7 +493,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
+              for (int hf = 0; hf < HF; ++hf)
                 if (!(seen[mt][hf] >> x & 1)) sc[mt][x >> 1][2 * hf + (x & 1)] = 0.f;
         }
 #pragma unroll
@@ -486,11 +501,12 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
+            for (int hf = 0; hf < HF; ++hf) {
               const float* z = sc[mt][nt] + 2 * hf;
               const uint32_t w = pack_bf16(z[0], z[1]);
               pa[mt][2 * nt + hf] = w;
-              if constexpr (kTwoTerms) pr[mt][2 * nt + hf] = pack_rest(z[0], z[1], w);
+              if constexpr (HF == 1) pa[mt][2 * nt + 1] = pack_rest(z[0], z[1], w);
+              else pr[mt][2 * nt + hf] = pack_rest(z[0], z[1], w);
             }
         // O += P C': lane's keys 2c, 2c + 1, 2c + 8, 2c + 9, coordinates g * D/8 ..
 #pragma unroll
@@ -518,7 +534,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
                 mma_bf16(o[mt][nt], pa[mt], b0, b1);
-                if constexpr (kTwoTerms) mma_bf16(o[mt][nt], pr[mt], b0, b1);
+                if constexpr (HF == 2) mma_bf16(o[mt][nt], pr[mt], b0, b1);
               }
             }
         }
@@ -532,7 +548,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int hf = 0; hf < HF; ++hf) {
         l[mt][hf] += __shfl_xor_sync(kFull, l[mt][hf], 1);
         l[mt][hf] += __shfl_xor_sync(kFull, l[mt][hf], 2);
         if (c == 0) {
@@ -547,7 +563,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
+          for (int hf = 0; hf < HF; ++hf) {
             const int r = mt * 16 + hf * 8 + g;
             float m = ml[r];
 #pragma unroll
@@ -562,7 +578,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
                 // column 2c + e of the 8-column tile nt holds byte nt of lane group 2c + e
                 constexpr int kTiles = S::slab_row / 8;
                 const int col = (nt / kTiles) * 128 + (2 * c + e) * kTiles + nt % kTiles;
-                const float v = f == 0.f ? 0.f : o[mt][nt][2 * hf + e] * f;
+                const float v = f == 0.f ? 0.f : (HF == 1 ? o[mt][nt][e] + o[mt][nt][2 + e] : o[mt][nt][2 * hf + e]) * f;
                 dst[col] = w ? dst[col] + v : v;
               }
           }
@@ -613,9 +629,9 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 // first cut of that item, the records of blocks i - 1 (its second), i, i + 1, ..
 // (their first) become the item's rows.  A warp takes a row: first the records'
 // maxima and sums, a lane each, then their value sums one by one.
-template <int D, int MT, typename T>
+template <int D, int R, typename T>
 __global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, const float* records, const Cut* cuts) {
-  using S = Shape<D, MT>;
+  using S = Shape<D, R>;
   asm volatile("griddepcontrol.wait;" ::: "memory");         // the main grid is done
   const int i = blockIdx.x + 1;
   const Cut cut = cuts[i];
@@ -662,8 +678,8 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, const float
 
 int padded(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-// rows of a block: 16 where a kv-head's rows fit in them (or d > 128, for the registers), else 32
-int row_tiles(int d, int64_t rows) { return rows <= 16 || d > 128 ? 1 : 2; }
+// rows of a block: 8 or 16 where a kv-head's rows fit in them (or d > 128, for the registers), else 32
+int block_rows(int d, int64_t rows) { return rows <= 8 ? 8 : rows <= 16 || d > 128 ? 16 : 32; }
 
 bool code_map(CUtensorMap* m, const int8_t* base, int d, int64_t rows, int box) {
   const EncodeTiledFn enc = encode_tiled_fn();
@@ -678,22 +694,22 @@ bool code_map(CUtensorMap* m, const int8_t* base, int d, int64_t rows, int box) 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int MT, typename T>
+template <int D, int R, typename T>
 int launch_shape(const TreeArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int box, int grid, bool merge,
                  void* workspace, cudaStream_t st) {
-  using S = Shape<D, MT>;
+  using S = Shape<D, R>;
   static_assert(S::bytes + 1024 <= 228 * 1024 / S::blocks_per_sm, "the blocks of an SM must fit");
-  int e = ensure_dyn_smem(reinterpret_cast<const void*>(tree_kernel<D, MT, T>), S::bytes);
+  int e = ensure_dyn_smem(reinterpret_cast<const void*>(tree_kernel<D, R, T>), S::bytes);
   if (e) return e;
   Cut* cuts = static_cast<Cut*>(workspace);
   float* records = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((size_t)grid * sizeof(Cut) + 255) / 256 * 256);
-  tree_kernel<D, MT, T><<<grid, S::threads, S::bytes, st>>>(km, vm, a, box, merge ? records : nullptr, merge ? cuts : nullptr);
+  tree_kernel<D, R, T><<<grid, S::threads, S::bytes, st>>>(km, vm, a, box, merge ? records : nullptr, merge ? cuts : nullptr);
   e = (int)cudaGetLastError();
   if (e || !merge) return e;
-  return launch_beside(tree_merge_kernel<D, MT, T>, dim3(grid - 1), 128, st, a, (const float*)records, (const Cut*)cuts);
+  return launch_beside(tree_merge_kernel<D, R, T>, dim3(grid - 1), 128, st, a, (const float*)records, (const Cut*)cuts);
 }
 
-int blocks_per_sm(int d, int mt) { return mt == 1 && d <= 128 ? 3 : 2; }
+int blocks_per_sm(int d, int rows) { return rows <= 16 && d <= 128 ? 3 : 2; }
 
 int tree_grid(const tq_ctx* h, int blocks_sm, int B, int Hkv, int64_t row_blocks, int64_t tiles) {
   const int64_t most = (int64_t)h->sm_count * blocks_sm;
@@ -708,8 +724,8 @@ size_t tree_workspace(const tq_ctx* h, int B, int n, int Hq, int Hkv) {
   if (B == 0 || n == 0 || Hq == 0) return 0;
   if (tree_tc_supported(h, n, Hq, Hkv)) return tree_tc_workspace(h, n, Hq, Hkv);
   const int64_t rows = (int64_t)n * (Hq / Hkv);
-  const int mt = row_tiles(h->d, rows), grid = h->sm_count * blocks_per_sm(h->d, mt);
-  return ((size_t)grid * sizeof(Cut) + 255) / 256 * 256 + (size_t)grid * 2 * 16 * mt * (padded(h->d) + 2) * 4;
+  const int R = block_rows(h->d, rows), grid = h->sm_count * blocks_per_sm(h->d, R);
+  return ((size_t)grid * sizeof(Cut) + 255) / 256 * 256 + (size_t)grid * 2 * R * (padded(h->d) + 2) * 4;
 }
 
 int launch_tree(const tq_ctx* h, const TreeArgs& a, int dtype, void* workspace, void* stream) {
@@ -720,24 +736,27 @@ int launch_tree(const tq_ctx* h, const TreeArgs& a, int dtype, void* workspace, 
   if (!code_map(&km, a.kcodes, h->d, a.rows, box) || !code_map(&vm, a.vcodes, h->d, a.rows, box))
     return (int)cudaErrorInvalidValue;
   const int64_t rows = (int64_t)a.n * (a.Hq / a.Hkv);
-  const int mt = row_tiles(h->d, rows);
-  const int64_t blocks = (rows + 16 * mt - 1) / (16 * mt), tiles = ((int64_t)a.max_pages * a.page + kKeys - 1) / kKeys;
+  const int R = block_rows(h->d, rows);
+  const int64_t blocks = (rows + R - 1) / R, tiles = ((int64_t)a.max_pages * a.page + kKeys - 1) / kKeys;
   const int64_t items = a.B * (int64_t)a.Hkv * blocks;
   const bool merge = tiles > 1;
-  const int per_sm = blocks_per_sm(h->d, mt);
+  const int per_sm = blocks_per_sm(h->d, R);
   int grid = tree_grid(h, per_sm, a.B, a.Hkv, blocks, tiles);
   if (!merge) grid = (int)std::min<int64_t>(items, (int64_t)h->sm_count * per_sm);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == TQ_BF16;
-#define TQ_TREE(D, MT)                                                                                      \
-  return bf ? launch_shape<D, MT, __nv_bfloat16>(a, km, vm, box, grid, merge && grid > 1, workspace, st)    \
-            : launch_shape<D, MT, __half>(a, km, vm, box, grid, merge && grid > 1, workspace, st)
-  switch (padded(h->d) + mt) {
-    case 65: TQ_TREE(64, 1);
-    case 66: TQ_TREE(64, 2);
-    case 129: TQ_TREE(128, 1);
-    case 130: TQ_TREE(128, 2);
-    default: TQ_TREE(256, 1);
+#define TQ_TREE(D, R)                                                                                       \
+  return bf ? launch_shape<D, R, __nv_bfloat16>(a, km, vm, box, grid, merge && grid > 1, workspace, st)    \
+            : launch_shape<D, R, __half>(a, km, vm, box, grid, merge && grid > 1, workspace, st)
+  switch (padded(h->d) + R) {
+    case 64 + 8: TQ_TREE(64, 8);
+    case 64 + 16: TQ_TREE(64, 16);
+    case 64 + 32: TQ_TREE(64, 32);
+    case 128 + 8: TQ_TREE(128, 8);
+    case 128 + 16: TQ_TREE(128, 16);
+    case 128 + 32: TQ_TREE(128, 32);
+    case 256 + 8: TQ_TREE(256, 8);
+    default: TQ_TREE(256, 16);
   }
 #undef TQ_TREE
 }
