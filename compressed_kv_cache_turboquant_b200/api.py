@@ -93,6 +93,8 @@ class Handle:
         self.ptr = ptr
         self.d, self.b, self.variant, self.bh = d, b, variant, bh
         self.bm = b - 1 if variant == TQ_PROD else b
+        # where its constants and status word are: the device that was current when it was made
+        self.device = torch.cuda.current_device() if ptr and torch.cuda.is_available() else -1
 
     @property
     def words(self) -> int:
@@ -338,11 +340,13 @@ def _stream_on(stream, t: torch.Tensor) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _same_device(first: torch.Tensor, *rest) -> None:
+def _same_device(h: Handle, first: torch.Tensor, *rest) -> None:
     try:
         dev = first.get_device()
         if dev < 0:
             raise ValueError("expected a CUDA tensor (this library has no CPU path)")
+        if dev != h.device and h.device >= 0:
+            raise ValueError(f"tensors on {first.device}, a handle of device {h.device}")
         for t in rest:
             if t is not None and t.get_device() != dev:
                 raise ValueError("expected a CUDA tensor (this library has no CPU path)" if t.get_device() < 0 else
@@ -402,7 +406,7 @@ def tq_quant_kv8(h: Handle, k: torch.Tensor, v, slots: torch.Tensor, kcodes: tor
     """Quantize the keys and values of n tokens, [n][Hkv][d] each (a token
     stride is allowed; v may be None), into cache rows slots [n][Hkv] (int64,
     negative: left out)."""
-    _same_device(k, v, slots, kcodes, kscales, vcodes, vscales)
+    _same_device(h, k, v, slots, kcodes, kscales, vcodes, vscales)
     if k.dim() != 3:
         raise ValueError(f"k: expected [tokens][heads][d], got {tuple(k.shape)}")
     n, Hkv = k.size(0), k.size(1)
@@ -424,7 +428,7 @@ def tq_dequant_kv8(h: Handle, slots: torch.Tensor, kcodes: torch.Tensor, kscales
                    k: torch.Tensor, v=None, stream=None) -> None:
     """Read cache rows slots [n] (int64; outside the cache: zeros) back into k
     and v, [n][d] each (v may be None)."""
-    _same_device(slots, kcodes, kscales, vcodes, vscales, k, v)
+    _same_device(h, slots, kcodes, kscales, vcodes, vscales, k, v)
     n, d = slots.numel(), h.d
     if slots.dtype is not torch.int64:
         raise ValueError(f"slots: expected int64, got {slots.dtype}")
@@ -472,7 +476,7 @@ def tq_attn_prompt(h: Handle, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     [total][Hkv][d] (bfloat16 or float16, a token stride allowed), sequence s in
     tokens cu_seqlens[s] .. cu_seqlens[s+1]-1 (int32 [nseq+1]); out
     [total][Hq][d], lse [total][Hq] float32.  h gives d: any handle."""
-    _same_device(q, k, v, cu_seqlens, out, lse, workspace)
+    _same_device(h, q, k, v, cu_seqlens, out, lse, workspace)
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k: expected [tokens][heads][d]")
     total, Hq, Hkv = q.shape[0], q.shape[1], k.shape[1]
@@ -504,7 +508,7 @@ def tq_attn_tree(h: Handle, q: torch.Tensor, Hkv: int, ctx_lens: torch.Tensor, b
     of them see, then draft_lens [B] (n each if None) drafted ones, of which
     token i sees those in its bits mask [B][n][ceil(n/32)] (int32; a chain if
     None); block_table is [B*Hkv][max_pages] int32."""
-    _same_device(q, ctx_lens, block_table, kcodes, kscales, vcodes, vscales, out, lse, mask, draft_lens, workspace)
+    _same_device(h, q, ctx_lens, block_table, kcodes, kscales, vcodes, vscales, out, lse, mask, draft_lens, workspace)
     if q.dim() != 4 or q.shape[3] != h.d:
         raise ValueError(f"q: expected [B][n][Hq][{h.d}], got {tuple(q.shape)}")
     B, n, Hq, d = q.shape

@@ -308,7 +308,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
     if (warp == 8) {
       // ---------------- TMA
       if (lane == 0) {
-        int st = 0;
+        int st = 0, queries = 0;
         bool ok = true;
         for (int i = 0; ok && item(i, it); ++i) {
           auto load = [&](const CUtensorMap* map, int j) -> bool {
@@ -323,6 +323,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
           if (i > 0 && !mbar_wait(q_free, (uint32_t)((i - 1) & 1))) ok = false;
           if (ok) {
             const int rows = a.G * a.tq;
+            ++queries;
             mbar_arrive_expect_tx(q_full, (uint32_t)((it.n[1] ? 2 : 1) * S::slabs * rows * 128));
             for (int t = 0; t < (it.n[1] ? 2 : 1); ++t)
               for (int sl = 0; sl < S::slabs; ++sl)
@@ -341,6 +342,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         // no copy may still be in flight when the block ends
         for (int x = st > S::stages ? st - S::stages : 0; x < st; ++x)
           if (!mbar_wait(&full[x % S::stages], (uint32_t)((x / S::stages) & 1))) atomicOr(a.status, kStatusTimeout);
+        if (queries && !mbar_wait(q_full, (uint32_t)((queries - 1) & 1))) atomicOr(a.status, kStatusTimeout);
       }
     } else if (warp == 9) {
       // ---------------- MMA

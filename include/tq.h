@@ -377,8 +377,11 @@ TQ_API size_t tq_attn_prefill_workspace(tq_handle hk, int B, int nq, int Hq, int
  *   out         dev out, [total][Hq][d] of `dtype`;  lse  dev out, [total][Hq]
  *               float32, or NULL.  Tokens of no sequence (before the first, behind
  *               the last) are neither read nor written
- *   workspace   dev scratch of at least tq_attn_prompt_workspace(...) bytes
- * An infinity or NaN in a key or value reaches only the tokens that see it.
+ *   workspace   dev scratch of at least tq_attn_prompt_workspace(...) bytes (0 for
+ *               none); calls that may overlap need one each
+ * An infinity or NaN in a key or value reaches only the tokens that see it; a
+ * token all of whose logits are -infinity gives out = 0 and lse = -infinity.
+ * Sums are float32 and run before the division: values above 2^90 may overflow.
  * Supported: Hq / Hkv <= 128, nseq <= TQ_MAX_SEQS, total <= 2^31 / 128.
  * Errors: TQ_EINVAL, TQ_EUNSUPPORTED, TQ_EALIGN, TQ_EWORKSPACE, TQ_ECUDA.
  */
@@ -576,6 +579,7 @@ TQ_API int tq_dequant_kv8(tq_handle h, int64_t n, const int64_t* slots, const in
  * are negative or pass the block table, and page ids outside the cache, count
  * as absent keys and set TQ_STATUS_RANGE.  Codes and scales of keys that a token
  * does not see have no part in its result, whatever they hold.
+ * Sums are float32 and run before the division: values above 2^90 may overflow.
  * Supported: n <= TQ_MAX_DRAFT, B <= TQ_MAX_SEQS, rows < 2^31 - 4096
  * (TQ_EUNSUPPORTED otherwise).
  * Errors: TQ_EINVAL, TQ_EUNSUPPORTED, TQ_EALIGN, TQ_EWORKSPACE, TQ_ECUDA.
