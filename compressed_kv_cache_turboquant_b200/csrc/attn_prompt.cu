@@ -14,7 +14,9 @@
 // Q and K tiles are shared-memory operands, S and O accumulate in tensor memory,
 // and P overwrites the first half of its S as the tensor-memory operand of the
 // value product.  The two row tiles take turns: while one's softmax runs on the
-// CUDA cores, the tensor cores work for the other.  P is the inputs' type (one
+// CUDA cores, the tensor cores work for the other.  At d <= 64, where O is half as
+// wide, P has columns of its own, and a tile's next logits are computed beside its
+// softmax (8192 tokens, 32 heads: 385 us; 427 with P in the place of S).  P is the inputs' type (one
 // rounding of 2^-9 or 2^-12 relative; l sums the unrounded weights).
 //
 // Warps (384 threads, one block per SM, persistent over the items):
@@ -49,7 +51,6 @@ using namespace attn;
 constexpr int kTile = 128;                 // rows of a row tile, keys of a key tile
 constexpr int kThreads = 384;
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;   // 2 x 208 + 88 = 3 x 168, the registers at launch
-constexpr uint32_t kColS = 0, kColO = 256; // S/P of tiles 0, 1 at 0, 128; O at 256, 384
 constexpr int kBadSlots = 8;               // items whose bad-key bits are kept (more than the ring can run ahead)
 constexpr int kBadTiles = 4;               // key tiles of an item that some row does not see whole: 3 at most
 constexpr int kBadWords = 4 + 4 * kBadTiles;   // what each scanning warp found in all (two words, two spare), then a bit per key
@@ -60,6 +61,11 @@ template <int D>
 struct Shape {
   static constexpr int slabs = D / 64;
   static constexpr int tile = kTile * D * 2;           // bytes of a Q, K or V tile
+  // tensor memory: S of the two row tiles; O; and for D = 64, where that leaves room, P
+  // apart from S, so that the next logits are under way while the softmax works
+  static constexpr bool apart = D == 64;
+  static constexpr uint32_t col_s = 0, col_p = apart ? 256 : 0, step_p = apart ? 64 : 128;
+  static constexpr uint32_t col_o = apart ? 384 : 256, step_o = apart ? 64 : 128;
   static constexpr int stages = D == 128 ? 4 : 8;
   static constexpr int off_ring = 2 * tile;
   static constexpr int off_out = off_ring + stages * tile;   // [8 warps][32 rows][128 bytes] results
@@ -208,10 +214,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   uint64_t* s_full = clean + S::stages;       // [2] MMA commit: logits of a tile
   uint64_t* p_ready = s_full + 2;        // [2][2] 4 softmax warps: weights of a tile's first, second 64 keys written
   uint64_t* pv_done = p_ready + 4;       // [2] MMA commit: value product done
-  uint64_t* done = pv_done + 2;
+  uint64_t* s_taken = pv_done + 2;       // [2] 4 softmax warps: logits of a tile read
+  uint64_t* done = s_taken + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   int4* direct_item = reinterpret_cast<int4*>(smem + S::off_bar + kBarBytes);
-  static_assert((3 * S::stages + 11) * 8 + 4 <= kBarBytes && S::bytes <= 232448, "shared memory");
+  static_assert((3 * S::stages + 13) * 8 + 4 <= kBarBytes && S::bytes <= 232448, "shared memory");
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -227,6 +234,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       mbar_init(&p_ready[2 * t], 4);
       mbar_init(&p_ready[2 * t + 1], 4);
       mbar_init(&pv_done[t], 1);
+      mbar_init(&s_taken[t], 4);
     }
     mbar_init(done, 1);
     fence_mbar_init();
@@ -347,16 +355,24 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
     } else if (warp == 9) {
       // ---------------- MMA
       constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+      constexpr uint32_t kColS = S::col_s, kColP = S::col_p, kColO = S::col_o;
       constexpr uint32_t idesc_s = idesc_f16(kTile, kTile, bf), idesc_o = idesc_f16(kTile, D, bf) | (1u << 16);
       const uint32_t lead = elect_one();
       const uint64_t qd = sw128_kmajor_desc(smem_u32(smem)), kd = sw128_kmajor_desc(smem_u32(ring));
       const uint64_t vd = sw128_mnmajor_desc(smem_u32(ring), kTile * 128);
       int st = 0, pv0 = 0, pv1 = 0;                         // ring steps; value products of tiles 0, 1 so far
+      int qk[2] = {0, 0};                                   // logit products of tiles 0, 1
       bool ok = true;
       auto wait_full = [&](int x) { return mbar_wait_warp(&full[x % S::stages], (uint32_t)((x / S::stages) & 1)); };
-      // S of tile t from the K tile of ring step x; the buffer's last P must have been consumed
+      // S of tile t from the K tile of ring step x; the buffer's last S must have been
+      // read, or the P that took its place consumed
       auto logits = [&](int t, int pv, int x) -> bool {
-        if (pv > 0 && !mbar_wait_warp(&pv_done[t], (uint32_t)((pv - 1) & 1))) return false;
+        if (S::apart) {
+          if (qk[t] > 0 && !mbar_wait_warp(&s_taken[t], (uint32_t)((qk[t] - 1) & 1))) return false;
+          ++qk[t];
+        } else {
+          if (pv > 0 && !mbar_wait_warp(&pv_done[t], (uint32_t)((pv - 1) & 1))) return false;
+        }
         tc_fence_after();
         const uint64_t q = qd + t * (S::tile >> 4), k = kd + (uint32_t)(x % S::stages) * (S::tile >> 4);
 #pragma unroll
@@ -376,7 +392,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
             if (!mbar_wait_warp(&p_ready[2 * t + ks / (kTile / 32)], (uint32_t)(pv & 1))) return false;
             tc_fence_after();
           }
-          mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + 8 * ks, v + ks * (2048 >> 4), idesc_o,
+          mma_ts(tmem + kColO + t * S::step_o, tmem + kColP + t * S::step_p + 8 * ks, v + ks * (2048 >> 4), idesc_o,
                  (first && ks == 0) ? 0u : 1u, lead);
         }
         commit(&pv_done[t], lead);
@@ -395,14 +411,25 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
           ok = wait_full(xv) && (j < cut || mbar_wait_warp(&clean[xv % S::stages], (uint32_t)((xv / S::stages) & 1)));
           if (!ok) break;
           const bool more = j + 1 < it.tiles;
-          if (j < it.n[0] && !(ok = values(0, pv0++, xv, j == 0))) break;
-          if (more && !(ok = wait_full(xk))) break;
-          if (j + 1 < it.n[0] && !(ok = logits(0, pv0, xk))) break;
-          if (j < it.n[1] && !(ok = values(1, pv1++, xv, j == 0))) break;
-          commit(&empty[xv % S::stages], lead);
-          if (j + 1 < it.n[1] && !(ok = logits(1, pv1, xk))) break;
-          if (more) commit(&empty[xk % S::stages], lead);
-          if (j + 2 == it.tiles) commit(q_free, lead);
+          if constexpr (S::apart) {
+            if (more && !(ok = wait_full(xk))) break;
+            if (j + 1 < it.n[0] && !(ok = logits(0, 0, xk))) break;
+            if (j < it.n[0] && !(ok = values(0, pv0++, xv, j == 0))) break;
+            if (j + 1 < it.n[1] && !(ok = logits(1, 0, xk))) break;
+            if (more) commit(&empty[xk % S::stages], lead);
+            if (j + 2 == it.tiles) commit(q_free, lead);
+            if (j < it.n[1] && !(ok = values(1, pv1++, xv, j == 0))) break;
+            commit(&empty[xv % S::stages], lead);
+          } else {
+            if (j < it.n[0] && !(ok = values(0, pv0++, xv, j == 0))) break;
+            if (more && !(ok = wait_full(xk))) break;
+            if (j + 1 < it.n[0] && !(ok = logits(0, pv0, xk))) break;
+            if (j < it.n[1] && !(ok = values(1, pv1++, xv, j == 0))) break;
+            commit(&empty[xv % S::stages], lead);
+            if (j + 1 < it.n[1] && !(ok = logits(1, pv1, xk))) break;
+            if (more) commit(&empty[xk % S::stages], lead);
+            if (j + 2 == it.tiles) commit(q_free, lead);
+          }
         }
         st += 2 * it.tiles;
       }
@@ -468,7 +495,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t sc = tmem + lanes + kColS + t * 128, oc = tmem + lanes + kColO + t * 128;
+    const uint32_t sc = tmem + lanes + S::col_s + t * 128, pc = tmem + lanes + S::col_p + t * S::step_p;
+    const uint32_t oc = tmem + lanes + S::col_o + t * S::step_o;
     const int row_tok = r / a.G, row_head = r % a.G;
     const int warp_tok = __shfl_sync(kFull, row_tok, 0);    // of the warp's first row
     const float cl = a.scale_log2;
@@ -490,6 +518,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) regs_after_wait(x[c]);
+        if (S::apart) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_taken[t]);
+        }
         // keys past the row's own take no part; a group of 32 that the warp's
         // first row sees whole needs no look
         const int lim = pos - j * kTile, low = it.tok[t] + warp_tok - j * kTile;
@@ -512,6 +545,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * cl;
         if (!(top < INFINITY)) l = NAN;                     // a seen logit is NaN or infinite: so is the row
         const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
+        // O and the weights' buffer are free once the value product of tile j - 1 is done
+        // (where these logits took the weights' place, it was done before them)
+        if (S::apart && j > 0) {
+          if (!(ok = mbar_wait_warp(&pv_done[t], (uint32_t)((steps - 1) & 1)))) break;
+          tc_fence_after();
+        }
         if (__any_sync(kFull, grow)) {
           float f = 1.f;
           if (grow) {
@@ -520,7 +559,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
             m = top;
           }
           if (j > 0) {
-            // the value product of tile j - 1 was done before this tile's logits began
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               float o[16];
@@ -554,7 +592,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
               sum[e & 1] = add2(sum[e & 1], pair(p0, p1));
               u[e] = pack(p0, p1, T());
             }
-            tmem_st16(sc + 16 * c, u);
+            tmem_st16(pc + 16 * c, u);
           }
           tmem_wait_st();
           tc_fence_before();
