@@ -30,8 +30,10 @@
 //             rows that do see them add them at the end (a bit per key)
 //
 // Items are sorted by length of their key range, longest first, by a one-block
-// kernel (prompt_plan_kernel); a grid with no more items than blocks finds them
-// itself.
+// kernel (prompt_plan_kernel), and a block takes the next one when it has loaded
+// its last tile (nine prompts of 8191 tokens, 16 heads of d = 64: 75 us; 86 with
+// the list dealt out beforehand).  A grid with no more items than blocks finds
+// them itself.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -55,7 +57,8 @@ constexpr int kBadSlots = 8;               // items whose bad-key bits are kept 
 constexpr int kBadTiles = 4;               // key tiles of an item that some row does not see whole: 3 at most
 constexpr int kBadWords = 4 + 4 * kBadTiles;   // what each scanning warp found in all (two words, two spare), then a bit per key
 constexpr int kBuckets = 1024;
-constexpr int kBarBytes = 320;             // room for the barriers and the tensor-memory address
+constexpr int kItemSlots = 4;              // items on their way to the warps
+constexpr int kBarBytes = 448;             // room for the barriers and the tensor-memory address
 
 template <int D>
 struct Shape {
@@ -71,7 +74,7 @@ struct Shape {
   static constexpr int off_out = off_ring + stages * tile;   // [8 warps][32 rows][128 bytes] results
   static constexpr int off_bad = off_out + 8 * 32 * 128;     // [kBadSlots][kBadWords]
   static constexpr int off_bar = off_bad + kBadSlots * kBadWords * 4;
-  static constexpr int bytes = off_bar + kBarBytes + 16 + 1024;
+  static constexpr int bytes = off_bar + kBarBytes + 16 * (1 + kItemSlots) + 1024;
 };
 
 struct PromptArgs {
@@ -80,7 +83,7 @@ struct PromptArgs {
   float* lse;
   const int32_t* cu;
   const int4* items;      // (first token, tokens, item of the sequence, 0), by key range
-  const int32_t* count;   // items
+  int32_t* count;         // items, then the next of all their heads that no block has taken
   int64_t v_stride;
   int total, nseq, Hq, Hkv, d, G, tq;   // tq = 128 / G tokens of a row tile
   int direct;             // no plan: block i finds item i / Hkv
@@ -119,7 +122,7 @@ struct Item {
 // as the nearest that do not, so the sequences never overlap and the list never
 // holds more than total / (2 tq) + nseq items.
 __global__ void __launch_bounds__(1024) prompt_plan_kernel(const int32_t* cu, int nseq, int total, int per_item,
-                                                           int4* items, int32_t* count) {
+                                                           int4* items, int32_t* count, int grid) {
   __shared__ int bound[4097];
   __shared__ int before[4097];              // items of the sequences before
   __shared__ int bucket[kBuckets];
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const int32_t* cu, in
     __syncthreads();
   }
   const int n = carry;
-  if (tid == 0) before[nseq] = n, *count = n;
+  if (tid == 0) before[nseq] = n, count[0] = n, count[1] = grid;
   bucket[tid] = 0;
   __syncthreads();
   // a bucket per key-range length (or so many of them alike that 1024 do)
@@ -215,10 +218,13 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   uint64_t* p_ready = s_full + 2;        // [2][2] 4 softmax warps: weights of a tile's first, second 64 keys written
   uint64_t* pv_done = p_ready + 4;       // [2] MMA commit: value product done
   uint64_t* s_taken = pv_done + 2;       // [2] 4 softmax warps: logits of a tile read
-  uint64_t* done = s_taken + 2;
+  uint64_t* item_full = s_taken + 2;     // [kItemSlots] the TMA warp
+  uint64_t* item_free = item_full + kItemSlots;   // [kItemSlots] every other warp at work
+  uint64_t* done = item_free + kItemSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   int4* direct_item = reinterpret_cast<int4*>(smem + S::off_bar + kBarBytes);
-  static_assert((3 * S::stages + 13) * 8 + 4 <= kBarBytes && S::bytes <= 232448, "shared memory");
+  int4* slots = direct_item + 1;         // [kItemSlots] (first token, tokens, item of the sequence or -1, kv-head)
+  static_assert((3 * S::stages + 13 + 2 * kItemSlots) * 8 + 4 <= kBarBytes && S::bytes <= 232448, "shared memory");
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -235,6 +241,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       mbar_init(&p_ready[2 * t + 1], 4);
       mbar_init(&pv_done[t], 1);
       mbar_init(&s_taken[t], 4);
+    }
+    for (int x = 0; x < kItemSlots; ++x) {
+      mbar_init(&item_full[x], 1);
+      mbar_init(&item_free[x], 8 + 1 + 2);
     }
     mbar_init(done, 1);
     fence_mbar_init();
@@ -278,25 +288,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   const uint32_t tmem = *tmem_slot;
 
   if (!a.direct) asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan is written
-  // the block's i-th item; every role walks the same ones
+  // The block's items: the TMA warp takes the next one of the list whenever it is
+  // about to run out, and tells the other warps
   const int all = a.direct ? 0 : __ldcg(a.count) * a.Hkv;
-  // (`ahead` holds the entry of item i, read an item earlier; ld.cg, since the
-  // plan may still be writing when this grid starts)
-  auto entry = [&](int i) -> int4 {
-    if (a.direct) return i == 0 ? *direct_item : make_int4(0, 0, -1, 0);
-    // there and back over the sorted list, so that the blocks' sums stay close
-    const int x = i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  auto entry = [&](int x) -> int4 {
     if (x >= all) return make_int4(0, 0, -1, 0);
-    int4 e = __ldcg(a.items + x / a.Hkv);
+    int4 e = __ldcg(a.items + x / a.Hkv);    // ld.cg: the plan may still be writing when this grid starts
     e.w = x % a.Hkv;
     return e;
   };
-  int4 ahead = entry(0);
-  auto item = [&](int i, Item& it) -> bool {
-    const int4 e = ahead;
-    if (e.z < 0) return false;
-    ahead = entry(i + 1);
-    it.h = a.direct ? blockIdx.x % a.Hkv : e.w;
+  auto unpack = [&](const int4& e, Item& it) {
+    it.h = e.w;
     it.start = e.x;
     it.len = e.y;
 #pragma unroll
@@ -305,6 +307,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       it.n[t] = it.tok[t] < it.len ? (min(it.tok[t] + a.tq, it.len) - 1) / kTile + 1 : 0;
     }
     it.tiles = max(it.n[0], it.n[1]);
+  };
+  auto item = [&](int i, Item& it, bool& ok) -> bool {
+    if (!ok || !(ok = mbar_wait_warp(&item_full[i % kItemSlots], (uint32_t)((i / kItemSlots) & 1)))) return false;
+    const int4 e = slots[i % kItemSlots];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_free[i % kItemSlots]);
+    if (e.z < 0) return false;
+    unpack(e, it);
     return true;
   };
   // the first key tile that some row of the item does not see whole
@@ -318,7 +328,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       if (lane == 0) {
         int st = 0, queries = 0;
         bool ok = true;
-        for (int i = 0; ok && item(i, it); ++i) {
+        int4 e = a.direct ? make_int4(direct_item->x, direct_item->y, direct_item->z, blockIdx.x % a.Hkv) : entry(blockIdx.x);
+        for (int i = 0;; ++i) {
+          ok = mbar_wait(&item_free[i % kItemSlots], (uint32_t)(((i / kItemSlots) & 1) ^ 1));
+          if (!ok) break;
+          slots[i % kItemSlots] = e;
+          mbar_arrive(&item_full[i % kItemSlots]);
+          if (e.z < 0) break;
+          unpack(e, it);
           auto load = [&](const CUtensorMap* map, int j) -> bool {
             const int s = st % S::stages;
             if (!mbar_wait(&empty[s], (uint32_t)(((st / S::stages) & 1) ^ 1))) return false;
@@ -338,13 +355,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
                 tma_load_3d(&qmap, q_full, smem + t * S::tile + sl * kTile * 128, sl * 64, it.h * a.G,
                             it.start + it.tok[t]);
           }
+          for (int j = 0; ok && j < it.tiles; ++j) ok = load(&kmap, j) && load(&vmap, j);
+          if (!ok) break;
+          e = a.direct ? make_int4(0, 0, -1, 0) : entry(atomicAdd(a.count + 1, 1));
           // the next item's queries cannot be loaded before this one's last logits:
           // have them on their way to L2 until then
-          if (ok && ahead.z >= 0)
+          if (e.z >= 0)
             for (int t = 0; t < 2; ++t)
               for (int sl = 0; sl < S::slabs; ++sl)
-                tma_prefetch_3d(&qmap, sl * 64, ahead.w * a.G, min(ahead.x + (ahead.z * 2 + t) * a.tq, a.total - 1));
-          for (int j = 0; ok && j < it.tiles; ++j) ok = load(&kmap, j) && load(&vmap, j);
+                tma_prefetch_3d(&qmap, sl * 64, e.w * a.G, min(e.x + (e.z * 2 + t) * a.tq, a.total - 1));
         }
         if (!ok) atomicOr(a.status, kStatusTimeout);
         // no copy may still be in flight when the block ends
@@ -398,7 +417,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         commit(&pv_done[t], lead);
         return true;
       };
-      for (int i = 0; ok && item(i, it); ++i) {
+      for (int i = 0; item(i, it, ok); ++i) {
         ok = mbar_wait_warp(q_full, (uint32_t)(i & 1)) && wait_full(st) && (!it.n[0] || logits(0, pv0, st)) &&
              (!it.n[1] || logits(1, pv1, st));
         if (!ok) break;
@@ -442,7 +461,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       const int w = warp - 10;
       int st = 0;
       bool ok = true;
-      for (int i = 0; ok && item(i, it); ++i) {
+      for (int i = 0; item(i, it, ok); ++i) {
         uint32_t* bits = bad + (i % kBadSlots) * kBadWords;
         uint32_t found = 0;
         const int cut = first_cut(it);
@@ -503,7 +522,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
     uint8_t* stage = smem + S::off_out + warp * 32 * 128;
     int steps = 0;
     bool ok = true;
-    for (int i = 0; ok && item(i, it); ++i) {
+    for (int i = 0; item(i, it, ok); ++i) {
       const int n = it.n[t];
       if (n == 0) continue;
       const int pos = it.tok[t] + row_tok;                  // the row's token in its sequence
@@ -739,10 +758,10 @@ int launch_prompt(const tq_ctx* h, const void* q, const void* k, const void* v, 
   const int64_t work = most_items(nseq, total, a.tq) * Hkv;
   a.direct = work <= h->sm_count;
   if (!a.direct) {
-    a.count = static_cast<const int32_t*>(workspace);
+    a.count = static_cast<int32_t*>(workspace);
     a.items = reinterpret_cast<const int4*>(static_cast<char*>(workspace) + 256);
     prompt_plan_kernel<<<1, 1024, 0, st>>>(cu, nseq, (int)total, 2 * a.tq, const_cast<int4*>(a.items),
-                                           const_cast<int32_t*>(a.count));
+                                           a.count, (int)std::min<int64_t>(work, h->sm_count));
     const int e = (int)cudaGetLastError();
     if (e) return e;
   }
