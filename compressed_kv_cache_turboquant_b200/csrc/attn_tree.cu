@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, const float
     float v[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) v[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int x = 0; x < n; ++x) {
       const float* p = rec(x);
       const float mx = __ldcg(p + D), f = mx == -INFINITY ? 0.f : ex2(mx - m);

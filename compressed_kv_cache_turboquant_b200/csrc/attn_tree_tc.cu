@@ -636,50 +636,107 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of the item that the main grid's block i (> 0) began inside of, if
-// i is the item's first cut: the second record of block i - 1 and the first ones of
-// i, i + 1, ..  Thread = row; blockIdx.y takes 16 of the coordinates.
-template <int D, int NT, typename T>
-__global__ void __launch_bounds__(NT * kTile) tree_tc_merge_kernel(const TcArgs ta) {
+// Joins the parts of an item that a cut divides: blocks begin .. end of the main grid
+// hold them, the first in its second record, the others in their first.  A block takes
+// some rows (z) and coordinates (y) of one.  Where there are many items, thread = row,
+// and blockIdx.x + 1 is the main grid's block whose cut it looks at (most are not an
+// item's first).  Few items have many records each: blockIdx.x counts the items, and
+// four slices of threads take every fourth record (8000 tokens of two heads in 63
+// records: 32 us, 40 with one slice; 64 sequences of 1000 tokens: 203 us, 185 with one).
+template <int kSlices, int NT>
+struct Merge {
+  static constexpr int rows = kSlices == 1 ? NT * kTile : 64, cols = kSlices == 1 ? 4 : 8;
+};
+
+template <int D, int NT, int kSlices, typename T>
+__global__ void __launch_bounds__(kSlices * Merge<kSlices, NT>::rows) tree_tc_merge_kernel(const TcArgs ta, int blocks) {
   using S = Shape<D, NT>;
+  constexpr int kRows = Merge<kSlices, NT>::rows, kCols = Merge<kSlices, NT>::cols, kWarps = kSlices * kRows / 32;
   const TreeArgs& a = ta.t;
+  __shared__ uint32_t first[kWarps];                         // bit: block i is the first cut of its item
+  __shared__ float part[kSlices > 1 ? kSlices : 1][kCols + 2][kSlices > 1 ? kRows : 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");         // the main grid is done
-  const int i = blockIdx.x + 1;
-  const Cut cut = ta.cuts[i];
-  if (cut.begin != i - 1) return;
-  const int last = cut.end;
-  const int t = threadIdx.x / kTile, row_tok = threadIdx.x % kTile / ta.G, row_head = threadIdx.x % kTile % ta.G;
+  const int tid = threadIdx.x, lane = tid & 31;
+  int at = blockIdx.x + 1;
+  if constexpr (kSlices > 1) {
+    int left = blockIdx.x;
+    at = -1;
+    for (int b0 = 1; b0 < blocks && at < 0; b0 += 32 * kWarps) {
+      const int i = b0 + tid;
+      const uint32_t m = __ballot_sync(kFull, i < blocks && __ldcg(&ta.cuts[i].begin) == i - 1);
+      if (b0 > 1) __syncthreads();
+      if (lane == 0) first[tid >> 5] = m;
+      __syncthreads();
+      for (int w = 0; w < kWarps && at < 0; ++w) {
+        uint32_t bits = first[w];
+        const int n = __popc(bits);
+        if (left >= n) {
+          left -= n;
+          continue;
+        }
+        while (left--) bits &= bits - 1;
+        at = b0 + 32 * w + __ffs(bits) - 1;
+      }
+    }
+    if (at < 0) return;                                      // fewer items are divided
+  }
+  const Cut cut = ta.cuts[at];
+  if (cut.begin != at - 1) return;
+  const int r = blockIdx.z * kRows + tid % kRows, slice = tid / kRows, c0 = blockIdx.y * kCols;
+  const int t = r / kTile, row_tok = r % kTile / ta.G, row_head = r % kTile % ta.G;
   const int tok = (cut.rb * NT + t) * ta.tq + row_tok;
   const int drafts = a.draft_lens ? min(max(__ldg(a.draft_lens + cut.b), 0), a.n) : a.n;
-  if (row_tok >= ta.tq || tok >= drafts) return;
-  auto rec = [&](int x) { return ta.records + ((int64_t)x * 2 + (x == i - 1 ? 1 : 0)) * (D + 2) * S::rows + threadIdx.x; };
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int x = i - 1; x <= last; ++x) m = fmaxf(m, __ldcg(rec(x) + (int64_t)D * S::rows));
-  float l = 0.f, v[16];
+  const bool live = row_tok < ta.tq && tok < drafts;
+  float m = -INFINITY, l = 0.f, v[kCols];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = 0.f;
-#pragma unroll 2
-  for (int x = i - 1; x <= last; ++x) {
-    const float* p = rec(x);
-    const float mx = __ldcg(p + (int64_t)D * S::rows), lx = __ldcg(p + (int64_t)(D + 1) * S::rows);
-    const float f = mx == -INFINITY ? 0.f : ex2(mx - m);
-    l += mx == -INFINITY ? lx : lx * f;                     // nothing seen: 0, or NaN
+  for (int e = 0; e < kCols; ++e) v[e] = 0.f;
+  if (live) {
+    auto rec = [&](int x) { return ta.records + ((int64_t)x * 2 + (x == cut.begin ? 1 : 0)) * (D + 2) * S::rows + r; };
+#pragma unroll 8
+    for (int x = cut.begin + slice; x <= cut.end; x += kSlices) m = fmaxf(m, __ldcg(rec(x) + (int64_t)D * S::rows));
+#pragma unroll 8
+    for (int x = cut.begin + slice; x <= cut.end; x += kSlices) {
+      const float* p = rec(x);
+      const float mx = __ldcg(p + (int64_t)D * S::rows), lx = __ldcg(p + (int64_t)(D + 1) * S::rows);
+      const float f = mx == -INFINITY ? 0.f : ex2(mx - m);
+      l += mx == -INFINITY ? lx : lx * f;                    // nothing seen: 0, or NaN
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float y = __ldcg(p + (int64_t)(blockIdx.y * 16 + e) * S::rows);
-      v[e] = f == 0.f ? v[e] : fmaf(y, f, v[e]);
+      for (int e = 0; e < kCols; ++e) {
+        const float y = __ldcg(p + (int64_t)(c0 + e) * S::rows);
+        v[e] = f == 0.f ? v[e] : fmaf(y, f, v[e]);
+      }
     }
   }
+  if constexpr (kSlices > 1) {
+    float (*mine)[kRows] = part[slice];
+    const int k = tid % kRows;
+    mine[0][k] = m;
+    mine[1][k] = l;
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) mine[2 + e][k] = v[e];
+    __syncthreads();
+    if (slice) return;
+#pragma unroll
+    for (int x = 1; x < kSlices; ++x) m = fmaxf(m, part[x][0][k]);
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) v[e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kSlices; ++x) {
+      const float mx = part[x][0][k], lx = part[x][1][k], f = mx == -INFINITY ? 0.f : ex2(mx - m);
+      l += mx == -INFINITY ? lx : lx * f;
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) v[e] = f == 0.f ? v[e] : fmaf(part[x][2 + e][k], f, v[e]);
+    }
+  }
+  if (!live) return;
   const int64_t row = ((int64_t)cut.b * a.n + tok) * a.Hq + cut.h * ta.G + row_head;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* out = static_cast<T*>(a.out) + row * a.d + blockIdx.y * 16;
-  if ((int)blockIdx.y * 16 < a.d) {
+  if (c0 < a.d) {
+    T* out = static_cast<T*>(a.out) + row * a.d + c0;
 #pragma unroll
-    for (int e = 0; e < 16; e += 8)
-      *reinterpret_cast<uint4*>(out + e) =
-          make_uint4(pack(v[e] * inv, v[e + 1] * inv, T()), pack(v[e + 2] * inv, v[e + 3] * inv, T()),
-                     pack(v[e + 4] * inv, v[e + 5] * inv, T()), pack(v[e + 6] * inv, v[e + 7] * inv, T()));
+    for (int e = 0; e < kCols; e += 4)
+      *reinterpret_cast<uint2*>(out + e) = make_uint2(pack(v[e] * inv, v[e + 1] * inv, T()), pack(v[e + 2] * inv, v[e + 3] * inv, T()));
   }
   if (a.lse && blockIdx.y == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
@@ -698,7 +755,7 @@ bool raw_map(CUtensorMap* m, const int8_t* base, int d, int64_t rows, int box) {
 }
 
 template <int D, int NT, typename T>
-int launch_shape(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, TcArgs ta, int grid, bool merge,
+int launch_shape(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, TcArgs ta, int grid, int merge,
                  void* workspace, cudaStream_t st) {
   using S = Shape<D, NT>;
   const int e = ensure_dyn_smem(reinterpret_cast<const void*>(tree_tc_kernel<D, NT, T>), S::bytes);
@@ -710,7 +767,12 @@ int launch_shape(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap
   tree_tc_kernel<D, NT, T><<<grid, kThreads, S::bytes, st>>>(qm, km, vm, ta);
   const int e2 = (int)cudaGetLastError();
   if (e2 || !merge) return e2;
-  return launch_beside(tree_tc_merge_kernel<D, NT, T>, dim3(grid - 1, D / 16), NT * kTile, st, ta);
+  constexpr int kSlices = 4;
+  if (merge * 4 < grid)                                      // more than four records an item
+    return launch_beside(tree_tc_merge_kernel<D, NT, kSlices, T>,
+                         dim3(merge, D / Merge<kSlices, NT>::cols, NT * kTile / Merge<kSlices, NT>::rows),
+                         kSlices * Merge<kSlices, NT>::rows, st, ta, grid);
+  return launch_beside(tree_tc_merge_kernel<D, NT, 1, T>, dim3(grid - 1, D / Merge<1, NT>::cols), NT * kTile, st, ta, grid);
 }
 
 int row_tiles(int64_t rows) { return rows <= kTile ? 1 : 2; }
@@ -743,7 +805,8 @@ int launch_tree_tc(const tq_ctx* h, const TreeArgs& a, int dtype, void* workspac
   const int64_t blocks = (a.n + nt * ta.tq - 1) / (nt * ta.tq), tiles = ((int64_t)a.max_pages * a.page + kTile - 1) / kTile;
   const int64_t items = (int64_t)a.B * a.Hkv * blocks;
   const int grid = (int)(items >= h->sm_count || tiles >= h->sm_count ? h->sm_count : std::min<int64_t>(h->sm_count, items * tiles));
-  const bool merge = tiles > 1 && grid > 1;
+  // items that may be divided
+  const int merge = tiles > 1 ? (int)std::min<int64_t>(items, grid - 1) : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 #define TQ_TREE(D, NT)                                                                       \
   return bf ? launch_shape<D, NT, __nv_bfloat16>(qm, km, vm, ta, grid, merge, workspace, st) \
