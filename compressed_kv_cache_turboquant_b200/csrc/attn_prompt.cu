@@ -33,7 +33,7 @@
 // kernel (prompt_plan_kernel), and a block takes the next one when it has loaded
 // its last tile (nine prompts of 8191 tokens, 16 heads of d = 64: 75 us; 86 with
 // the list dealt out beforehand).  A grid with no more items than blocks finds
-// them itself.
+// them itself (six prompts of 331 tokens: 14.2 us, 17.2 with the list).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -65,14 +65,16 @@ struct Shape {
   static constexpr int stage = 2 * codes;                  // K and V codes (the swizzle repeats every 1024 bytes)
   static constexpr int scales = 2 * kKeys * 4;             // their scales
   static constexpr int ksteps = D / 16;
-  // 16 rows of up to 128 coordinates fit 128 registers a thread (with the query
-  // fragments in shared memory): three blocks of five warps on an SM.  Wider ones
-  // take two blocks of two warpgroups, of which the consumers' takes registers
-  // that the other, a single warp of which feeds the ring, gives back.
+  // 16 rows of up to 128 (64) coordinates fit 128 (96) registers a thread (with the
+  // query fragments in shared memory): three (four) blocks of five warps on an SM.
+  // Wider ones take two blocks of two warpgroups, of which the consumers' takes
+  // registers that the other, a single warp of which feeds the ring, gives back.
+  // 16 sequences of 16000 tokens, 8 kv-heads, 4 rows each: d = 128 149 us (173 with two
+  // wide blocks), d = 64 106 us (118 with three slim blocks, 114 with five, 155 wide).
   static constexpr bool slim = R <= 16 && D <= 128;
-  static constexpr int blocks_per_sm = slim ? 3 : 2;
+  static constexpr int blocks_per_sm = slim ? (D == 64 ? 4 : 3) : 2;
   static constexpr int threads = (slim ? kWarps + 1 : 2 * kWarps) * 32;
-  static constexpr int stages = D == 256 ? 2 : D == 128 ? (slim ? 3 : 5) : (slim ? 6 : 8);
+  static constexpr int stages = D == 256 ? 2 : D == 128 ? (slim ? 3 : 5) : (slim ? 5 : 8);
   static constexpr bool q_in_regs = !slim && MT * ksteps <= 8;
   static constexpr int off_scales = stages * stage;
   static constexpr int off_acc = off_scales + stages * scales;   // [rows][D + 4] merged value sums
@@ -678,7 +680,9 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, const float
 
 int padded(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-// rows of a block: 8 or 16 where a kv-head's rows fit in them (or d > 128, for the registers), else 32
+// rows of a block: 8 or 16 where a kv-head's rows fit in them (or d > 128, for the
+// registers), else 32.  4 rows of 16 x 16000 keys: 149 us in blocks of 8, 164 of 16;
+// 32 rows of 32 x 4000 keys: 166 us in one block of 32, 181 in two of 16
 int block_rows(int d, int64_t rows) { return rows <= 8 ? 8 : rows <= 16 || d > 128 ? 16 : 32; }
 
 bool code_map(CUtensorMap* m, const int8_t* base, int d, int64_t rows, int box) {
@@ -709,7 +713,7 @@ int launch_shape(const TreeArgs& a, const CUtensorMap& km, const CUtensorMap& vm
   return launch_beside(tree_merge_kernel<D, R, T>, dim3(grid - 1), 128, st, a, (const float*)records, (const Cut*)cuts);
 }
 
-int blocks_per_sm(int d, int rows) { return rows <= 16 && d <= 128 ? 3 : 2; }
+int blocks_per_sm(int d, int rows) { return rows <= 16 && d <= 128 ? (d <= 64 ? 4 : 3) : 2; }
 
 int tree_grid(const tq_ctx* h, int blocks_sm, int B, int Hkv, int64_t row_blocks, int64_t tiles) {
   const int64_t most = (int64_t)h->sm_count * blocks_sm;

@@ -292,7 +292,8 @@ struct TreeArgs {
 };
 size_t tree_workspace(const tq_ctx* h, int B, int n, int Hq, int Hkv);
 int launch_tree(const tq_ctx* h, const TreeArgs& a, int dtype, void* workspace, void* stream);
-// more rows of a kv-head than this take the tcgen05 kernel
+// more rows of a kv-head than this take the tcgen05 kernel: 32 rows of 32 x 4000 keys,
+// 8 kv-heads, 166 us on mma.sync and 177 on tcgen05, 36 rows 271 and 177
 constexpr int kTreeTcRows = 32;
 bool tree_tc_supported(const tq_ctx* h, int n, int Hq, int Hkv);
 size_t tree_tc_workspace(const tq_ctx* h, int n, int Hq, int Hkv);
