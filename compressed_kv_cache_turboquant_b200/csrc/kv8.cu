@@ -13,14 +13,16 @@
 // decides there.  A row that holds an infinity or a NaN has no such codes: it
 // gets s = NaN and codes 0, so that what reads it gets NaN in that row alone.
 //
-// Both directions are bound by HBM: d e + d + 4 bytes a row and tensor, plus 8
-// of the slot list (e: bytes of an element of x).  A thread takes two pieces of
-// eight elements, `lanes` pieces apart, so that neighbouring lanes read and
-// write neighbouring 16 (or 8) bytes, of each of two rows, whose loads are in
-// flight together; what a row needs once (its maximum, its scale, 1 / s) is
-// spread over sixteen elements.  65537 tokens of 8 kv-heads, d = 128, bf16 (keys and
-// values): written in 99.5 us, 4130 GB/s of 6560 (with one, four or eight rows a
-// thread 110 to 184); 2^20 rows are read in 147.7 us, 5570 GB/s (169 to 214).
+// Reading is bound by HBM, writing by its instructions (16 an element, issue slots
+// 70 % busy): d e + d + 4 bytes a row and tensor, plus 8 of the slot list (e: bytes of
+// an element of x).  A thread takes two pieces of eight elements, `lanes` pieces
+// apart, so that neighbouring lanes read and write neighbouring 16 (or 8) bytes, of
+// each of two rows, whose loads are in flight together; what a row needs once (its
+// maximum, its scale, 1 / s) is spread over sixteen elements.  65537 tokens of 8
+// kv-heads, d = 128, bf16 (keys and values) are written in 87 us, 4730 GB/s of 6560
+// (99 with the threads of a row and the heads not known to the compiler or divided
+// beforehand; with one, four or eight rows a thread 1.1 to 1.8 times as long); 2^20
+// rows are read in 143 us, 5750 GB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -49,6 +51,8 @@ struct Kv8Args {
   int64_t N;               // rows: tokens x heads
   int64_t rows;            // rows of the cache
   int Hkv, d;
+  uint32_t hkv_mul;        // n / Hkv = n hkv_mul >> hkv_shift for n < 2^31
+  int hkv_shift;
   int* status;
 };
 
@@ -212,8 +216,8 @@ __device__ __forceinline__ void codes_of(const float (&v)[8], float s, uint32_t 
 
 // lanes: threads of a row (a power of two >= d / 16), so that a row never
 // crosses a warp; pieces past d / 8 only take part in the shuffles
-template <typename T>
-__global__ void __launch_bounds__(kThreads) kv8_write_kernel(Kv8Args a, int lanes) {
+template <typename T, int lanes>
+__global__ void __launch_bounds__(kThreads) kv8_write_kernel(Kv8Args a) {
   const int which = blockIdx.y;
   const int sub = threadIdx.x & (lanes - 1);
   const int groups = kThreads / lanes;
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(Kv8Args a, int lane
     raw[i][0] = raw[i][1] = zero_raw<T>();
     if (n < a.N) {
       slot[i] = __ldg(a.slots + n);
-      const uint32_t t = (uint32_t)n / (uint32_t)a.Hkv, h = (uint32_t)n - t * (uint32_t)a.Hkv;
+      const uint32_t t = (uint32_t)((uint64_t)(uint32_t)n * a.hkv_mul >> a.hkv_shift), h = (uint32_t)n - t * (uint32_t)a.Hkv;
       const T* row = x + (int64_t)t * x_stride + (int64_t)h * a.d;
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -242,6 +246,7 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(Kv8Args a, int lane
 #pragma unroll
   for (int i = 0; i < kRowsPerThread; ++i) {
     uint32_t top = max_bits<T>(raw_max(raw[i][1], raw_max(raw[i][0], 0u)));
+#pragma unroll
     for (int m = lanes >> 1; m; m >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
     const bool finite = top < 0x7F800000u;
     const float s = finite ? scale_of(__uint_as_float(top)) : __uint_as_float(0x7FC00000u);
@@ -335,15 +340,26 @@ int launch_kv8_write(const tq_ctx* h, const void* k, const void* v, int dtype, i
   a.slots = slots;
   a.x_stride[0] = k_stride, a.x_stride[1] = v_stride;
   a.N = n * Hkv, a.rows = rows, a.Hkv = Hkv, a.d = h->d, a.status = h->dev.status;
+  // Granlund and Montgomery's division by an invariant integer: ceil(2^shift / Hkv), 2^(shift - 31) >= Hkv
+  a.hkv_shift = 31;
+  while ((1ll << (a.hkv_shift - 31)) < Hkv) ++a.hkv_shift;
+  a.hkv_mul = (uint32_t)(((1ull << a.hkv_shift) + Hkv - 1) / (uint64_t)Hkv);
   const int lanes = lanes_of(h->d), per = kThreads / lanes * kRowsPerThread;
   const dim3 grid((unsigned)((a.N + per - 1) / per), v ? 2 : 1);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == TQ_F32)
-    kv8_write_kernel<float><<<grid, kThreads, 0, st>>>(a, lanes);
-  else if (dtype == TQ_BF16)
-    kv8_write_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, lanes);
-  else
-    kv8_write_kernel<__half><<<grid, kThreads, 0, st>>>(a, lanes);
+  const auto launch = [&](auto type) {
+    using T = decltype(type);
+    switch (lanes) {
+      case 1: kv8_write_kernel<T, 1><<<grid, kThreads, 0, st>>>(a); break;
+      case 2: kv8_write_kernel<T, 2><<<grid, kThreads, 0, st>>>(a); break;
+      case 4: kv8_write_kernel<T, 4><<<grid, kThreads, 0, st>>>(a); break;
+      case 8: kv8_write_kernel<T, 8><<<grid, kThreads, 0, st>>>(a); break;
+      default: kv8_write_kernel<T, 16><<<grid, kThreads, 0, st>>>(a);
+    }
+  };
+  if (dtype == TQ_F32) launch(float());
+  else if (dtype == TQ_BF16) launch(__nv_bfloat16());
+  else launch(__half());
   return (int)cudaGetLastError();
 }
 
