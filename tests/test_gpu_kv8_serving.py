@@ -185,3 +185,51 @@ def test_workspaces_that_are_too_small_are_refused(n):
         c.run(workspace=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
     c.run(workspace=torch.empty(need, dtype=torch.uint8, device=DEV))
     c.check()
+
+
+@pytest.mark.parametrize("d", [8, 24, 72, 120])
+def test_prompts_of_a_compressed_cache_handle(d):
+    """Prompt attention takes the handle that compresses the same heads, whose dimension is any multiple of 8."""
+    h = Instance(d, 3, tq.TQ_MSE, seed=4).h
+    g = torch.Generator(device=DEV).manual_seed(d)
+    q = torch.randn(333, 6, d, generator=g, device=DEV).to(BF)
+    k, v = (torch.randn(333, 2, d, generator=g, device=DEV).to(BF) for _ in range(2))
+    cu = torch.tensor([0, 3, 3, 200, 333], dtype=torch.int32, device=DEV)
+    out, lse = torch.full_like(q, 77), torch.full((333, 6), 77.0, device=DEV)
+    tq.tq_attn_prompt(h, q, k, v, cu, d ** -0.5, out, lse=lse)
+    check_prompt(q, k, v, cu, d ** -0.5, out, lse)
+    assert tq.tq_device_status(h) == 0
+
+
+def test_prompt_graphs_that_share_a_workspace():
+    """Two captured calls with a list of items (more of them than blocks) and one workspace, replayed in turn."""
+    Hq, Hkv, d, scale = 32, 8, 64, 0.125
+    h = tq.tq_create_kv8(d)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    calls = []
+    sizes = ([700, 1, 2300, 64], [5, 1500, 1500])
+    ws = torch.empty(max(tq.tq_attn_prompt_workspace(h, len(x), sum(x), Hq, Hkv) for x in sizes), dtype=torch.uint8, device=DEV)
+    assert ws.numel() > 0
+    for lens in sizes:
+        n = sum(lens)
+        q = torch.randn(n, Hq, d, generator=g, device=DEV).to(HF)
+        k, v = (torch.randn(n, Hkv, d, generator=g, device=DEV).to(HF) for _ in range(2))
+        cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=DEV)
+        out = torch.zeros_like(q)
+        args = (h, q, k, v, cu, scale, out)
+        tq.tq_attn_prompt(*args, workspace=ws)
+        want = out.clone()
+        check_prompt(q, k, v, cu, scale, out, None, rows=[(0, 3), (640, 650), (1490, 1500), (2290, 2300)])
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            tq.tq_attn_prompt(*args, workspace=ws)
+        calls.append((graph, out, want, args))
+    for _ in range(3):
+        for graph, out, want, _ in calls:
+            out.zero_()
+            graph.replay()
+        for _, out, want, _ in calls:
+            assert torch.equal(out, want)
+    assert tq.tq_device_status(h) == 0
