@@ -372,25 +372,26 @@ def _token_rows(t: torch.Tensor, name: str, heads: int, d: int) -> int:
     """Checks [tokens][heads][d] with whole heads side by side; returns the
     elements from one token to the next (a slice of a fused projection has more
     than heads d of them)."""
-    if t.dim() != 3 or t.size(1) != heads or t.size(2) != d:
-        raise ValueError(f"{name}: expected [tokens][{heads}][{d}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{name}: expected [tokens][{heads}][{d}], got {tuple(shape)}")
     if t.is_contiguous():
         return heads * d
     if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
         raise ValueError(f"{name}: the heads of a token must lie side by side")
-    return t.stride(0) if t.size(0) > 1 else heads * d
+    return t.stride(0) if shape[0] > 1 else heads * d
 
 
 def _cache_rows(h: Handle, kcodes, kscales, vcodes, vscales) -> int:
     """Checks the four cache arrays (the values' may be None); returns their rows."""
-    rows, d = kcodes.size(0), h.d
-    for codes, scales in ((kcodes, kscales), (vcodes, vscales)):
-        if codes is None and scales is None and codes is not kcodes:
-            continue
-        if codes is None or codes.dtype is not torch.int8 or codes.dim() != 2 or codes.size(0) != rows or codes.size(1) != d:
-            raise ValueError(f"codes: expected int8 [rows][{d}], the same rows for keys and values")
-        if scales is None or scales.dtype is not torch.float32 or scales.dim() != 1 or scales.size(0) != rows:
-            raise ValueError("scales: expected float32 [rows], as many as the codes")
+    rows = kcodes.size(0)
+    shape, flat, int8, f32 = (rows, h.d), (rows,), torch.int8, torch.float32
+    if (kcodes.dtype is not int8 or kcodes.shape != shape or
+            (vcodes is not None and (vcodes.dtype is not int8 or vcodes.shape != shape))):
+        raise ValueError(f"codes: expected int8 [rows][{h.d}], the same rows for keys and values")
+    if (kscales is None or kscales.dtype is not f32 or kscales.shape != flat or (vscales is None) != (vcodes is None) or
+            (vscales is not None and (vscales.dtype is not f32 or vscales.shape != flat))):
+        raise ValueError("scales: expected float32 [rows], as many as the codes")
     return rows
 
 
