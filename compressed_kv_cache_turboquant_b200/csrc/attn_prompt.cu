@@ -34,7 +34,7 @@
 // row tile's own half value product (256), logits (512) and two hand-offs between
 // the warps (330 each), which its softmax cannot overlap while P takes the place of
 // S.  8192 tokens, 32 heads, d = 128: 0.478 ms, 1150 TFLOP/s of 1654 that the
-// library's matrix product reaches; 32768 tokens 8.25 ms, 1066.
+// library's matrix product reaches; 32768 tokens 8.28 ms, 1062.
 //
 // Items are sorted by length of their key range, longest first, by a one-block
 // kernel (prompt_plan_kernel), and a block takes the next one when it has loaded
