@@ -385,7 +385,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
               sc[key] = ksc * a.scale_log2;
               sc[kTile + key] = vsc;
               const uint32_t bits = __ballot_sync(kFull, there);
-              const bool odd = __any_sync(kFull, !(vsc < INFINITY));
+              const bool odd = __any_sync(kFull, !(fabsf(vsc) < INFINITY));
               if (lane == 0) {
                 uint32_t* to = reinterpret_cast<uint32_t*>(smem + S::off_valid) + (kt & 3) * 8 + w;
                 to[0] = bits;
