@@ -16,8 +16,12 @@
 // value product.  The two row tiles take turns: while one's softmax runs on the
 // CUDA cores, the tensor cores work for the other.  At d <= 64, where O is half as
 // wide, P has columns of its own, and a tile's next logits are computed beside its
-// softmax (8192 tokens, 32 heads: 385 us; 427 with P in the place of S).  P is the inputs' type (one
-// rounding of 2^-9 or 2^-12 relative; l sums the unrounded weights).
+// softmax (8192 tokens, 32 heads: 385 us; 427 with P in the place of S).  P is the inputs' type: one
+// rounding of 2^-9 or 2^-12 relative (l sums the unrounded weights).  float16's range is
+// short, so its weights are 2^7 larger (m lies 7 below the largest logit; O, l and lse
+// follow): they reach 2^15 of 65504, and only below 2^-21 of the reference become
+// subnormal, off by up to 2^-32 of it.  Without the 2^7 it was 2^-25: behind one
+// dominant key, a tail of 131071 keys of 2^-25.2 each (2^-8.2 of the row together) was lost.
 //
 // Warps (384 threads, one block per SM, persistent over the items):
 //   0-3, 4-7  softmax of row tile 0, 1: thread = row (TMEM lane); the reference
@@ -104,11 +108,22 @@ struct Bits;   // exponent bits of a 16-bit element, and what lifts them into th
 template <>
 struct Bits<__nv_bfloat16> {
   static constexpr uint32_t exponent = 0x7F807F80u, one = 0x00800080u;
+  static constexpr float raise = 0.f;   // weights are 2^raise times 2^(logit - the reference's)
 };
 template <>
 struct Bits<__half> {
   static constexpr uint32_t exponent = 0x7C007C00u, one = 0x04000400u;
+  static constexpr float raise = 7.f;
 };
+
+// two weights in the operand's type.  float16: the largest finite number for what would
+// pass it, which logits of 2^24 and more can, whose own float32 rounding is 1 and more
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi, __nv_bfloat16) { return pack_bf16(lo, hi); }
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi, __half) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
 
 // sign bits of the halves that are infinite or NaN
 template <typename T>
@@ -570,7 +585,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         }
         const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * cl;
         if (!(top < INFINITY)) l = NAN;                     // a seen logit is NaN or infinite: so is the row
-        const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
+        const bool grow = top > m + (kLazy + Bits<T>::raise) || (m == -INFINITY && top > m);
         // O and the weights' buffer are free once the value product of tile j - 1 is done
         // (where these logits took the weights' place, it was done before them)
         if (S::apart && j > 0) {
@@ -580,9 +595,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         if (__any_sync(kFull, grow)) {
           float f = 1.f;
           if (grow) {
-            f = m == -INFINITY ? 0.f : ex2(m - top);
+            const float next = top - Bits<T>::raise;
+            f = m == -INFINITY ? 0.f : ex2(m - next);
             l *= f;
-            m = top;
+            m = next;
           }
           if (j > 0) {
 #pragma unroll 1
@@ -616,7 +632,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
               unpair(z, p0, p1);
               p0 = ex2(p0), p1 = ex2(p1);
               sum[e & 1] = add2(sum[e & 1], pair(p0, p1));
-              u[e] = pack(p0, p1, T());
+              u[e] = pack_weights(p0, p1, T());
             }
             tmem_st16(pc + 16 * c, u);
           }

@@ -382,6 +382,8 @@ TQ_API size_t tq_attn_prefill_workspace(tq_handle hk, int B, int nq, int Hq, int
  * An infinity or NaN in a key or value reaches only the tokens that see it; a
  * token all of whose logits are -infinity gives out = 0 and lse = -infinity.
  * Sums are float32 and run before the division: values above 2^90 may overflow.
+ * The softmax weights enter the value product rounded to `dtype`; a float16 one
+ * is off by 2^-12 of itself or 2^-32 of the row's largest weight, whichever is more.
  * Supported: Hq / Hkv <= 128, nseq <= TQ_MAX_SEQS, total <= 2^31 / 128.
  * Errors: TQ_EINVAL, TQ_EUNSUPPORTED, TQ_EALIGN, TQ_EWORKSPACE, TQ_ECUDA.
  */
