@@ -422,6 +422,9 @@ extern "C" int tq_create_kv8(tq_handle* out, int d) {
     h->block_bytes = 256;
     e = cudaMalloc(&h->block, h->block_bytes);
     if (e == cudaSuccess) e = cudaMemset(h->block, 0, h->block_bytes);
+    // a memset does not wait, and other streams do not wait for it: without this it could
+    // clear what the first call on one of them reports
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
     h->dev.status = static_cast<int*>(h->block);
   }
   if (e != cudaSuccess) {
