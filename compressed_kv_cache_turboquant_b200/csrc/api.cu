@@ -481,8 +481,14 @@ extern "C" int tq_destroy(tq_handle h) {
 
 extern "C" int tq_device_status(tq_handle h, int* status) {
   if (!h || !status) return set_error(TQ_EINVAL, "tq_device_status: NULL argument");
-  int e = cudaMemcpy(status, h->dev.status, sizeof(int), cudaMemcpyDeviceToHost);
+  // the copy alone waits for the streams that wait for the default one, which is not all of
+  // them; and the clearing has to be over before a later call can set a bit
+  DeviceGuard guard(h->device);
+  int e = guard.error;
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(status, h->dev.status, sizeof(int), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess) e = cudaMemset(h->dev.status, 0, sizeof(int));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
   return e ? cuda_error("tq_device_status", e) : clear_error();
 }
 

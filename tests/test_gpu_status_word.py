@@ -1,5 +1,6 @@
-"""The status word holds what the calls on a handle met, whichever streams they ran
-on: the handle's creation is complete when it returns."""
+"""The status word holds what the calls on a handle met: the handle's creation is
+complete when it returns, and reading the word waits for the device, whichever
+streams the calls ran on."""
 import pytest
 import torch
 
@@ -35,3 +36,17 @@ def test_a_handle_is_ready_when_its_creation_returns():
     side.synchronize()
     torch.cuda.synchronize()
     assert tq.tq_device_status(h) == tq.TQ_STATUS_RANGE
+
+
+def test_reading_the_word_waits_for_work_on_other_streams():
+    a, side = Arrays(), torch.cuda.Stream()
+    h = tq.tq_create_kv8(D)
+    a.write(h, side)
+    side.synchronize()
+    assert tq.tq_device_status(h) == tq.TQ_STATUS_RANGE
+    assert tq.tq_device_status(h) == 0
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(LONG)
+    a.write(h, side)
+    assert tq.tq_device_status(h) == tq.TQ_STATUS_RANGE
+    assert tq.tq_device_status(h) == 0
