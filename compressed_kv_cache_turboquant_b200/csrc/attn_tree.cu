@@ -694,7 +694,7 @@ bool code_map(CUtensorMap* m, const int8_t* base, int d, int64_t rows, int box) 
   const EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return false;
   const int D = padded(d);
-  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)std::max<int64_t>(rows, 1)};
   cuuint64_t strides[1] = {(cuuint64_t)d};
   cuuint32_t boxd[2] = {(cuuint32_t)(D > 128 ? 128 : D), (cuuint32_t)box};
   cuuint32_t es[2] = {1, 1};
@@ -803,7 +803,7 @@ extern "C" int tq_attn_tree(tq_handle h, const void* q, int dtype, int64_t q_str
   if (B == 0 || n == 0 || Hq == 0) return clear_error();
   if ((int64_t)B * n > 1 && (q_stride < (int64_t)Hq * h->d || q_stride % 8 != 0))
     return set_error(TQ_EINVAL, "%s: q_stride %lld (need >= Hq d and a multiple of 8)", fn, (long long)q_stride);
-  if (!q || !ctx_lens || !block_table || !kcodes || !kscales || !vcodes || !vscales || !out)
+  if (!q || !ctx_lens || !block_table || !out || (rows > 0 && (!kcodes || !kscales || !vcodes || !vscales)))
     return set_error(TQ_EINVAL, "%s: NULL pointer", fn);
   for (const void* p : {q, (const void*)ctx_lens, (const void*)draft_lens, (const void*)mask, (const void*)block_table,
                         (const void*)kcodes, (const void*)kscales, (const void*)vcodes, (const void*)vscales,
@@ -817,6 +817,10 @@ extern "C" int tq_attn_tree(tq_handle h, const void* q, int dtype, int64_t q_str
   a.ctx_lens = ctx_lens, a.draft_lens = draft_lens, a.mask = mask, a.block_table = block_table;
   a.max_pages = max_pages, a.page = page_size;
   a.kcodes = kcodes, a.kscales = kscales, a.vcodes = vcodes, a.vscales = vscales, a.rows = rows;
+  if (rows == 0) {
+    // no page id lies in it and nothing is loaded, but the tensor maps need an address and a row
+    a.kcodes = a.vcodes = static_cast<const int8_t*>(q);
+  }
   a.scale_log2 = scale * 1.4426950408889634f;
   a.out = out, a.lse = lse, a.status = h->dev.status;
   DeviceGuard guard(h->device);

@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(kSlices * Merge<kSlices, NT>::rows) tree_tc_me
 bool raw_map(CUtensorMap* m, const int8_t* base, int d, int64_t rows, int box) {
   const EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)std::max<int64_t>(rows, 1)};
   cuuint64_t strides[1] = {(cuuint64_t)d};
   cuuint32_t boxd[2] = {(cuuint32_t)(d <= 64 ? 64 : 128), (cuuint32_t)box};
   cuuint32_t es[2] = {1, 1};

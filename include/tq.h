@@ -571,7 +571,7 @@ TQ_API int tq_dequant_kv8(tq_handle h, int64_t n, const int64_t* slots, const in
  *                or NULL: a chain (token i sees j <= i)
  *   block_table  dev in, [B*Hkv][max_pages] int32 as in tq_attn_decode_paged;
  *                page_size a multiple of 8
- *   kcodes, kscales, vcodes, vscales   dev in, the cache (`rows` rows)
+ *   kcodes, kscales, vcodes, vscales   dev in, the cache (`rows` rows; may be NULL for 0)
  *   scale        logit scale, >= 0
  *   out          dev out, [B][n][Hq][d] of `dtype`;  lse  dev out, [B][n][Hq]
  *                float32, or NULL
