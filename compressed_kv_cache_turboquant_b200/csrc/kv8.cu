@@ -394,7 +394,8 @@ namespace {
 int check_kv8(const char* fn, int64_t rows, const void* kcodes, const void* kscales, const void* vcodes,
               const void* vscales, bool values) {
   if (rows < 0) return set_error(TQ_EINVAL, "%s: rows < 0", fn);
-  if (!kcodes || !kscales || (values && (!vcodes || !vscales))) return set_error(TQ_EINVAL, "%s: NULL pointer", fn);
+  // arrays of no rows need no address: no slot lies in them
+  if (rows > 0 && (!kcodes || !kscales || (values && (!vcodes || !vscales)))) return set_error(TQ_EINVAL, "%s: NULL pointer", fn);
   return TQ_OK;
 }
 

@@ -528,8 +528,8 @@ TQ_API int tq_create_kv8(tq_handle* h, int d);
  *             keys and values alike; a negative slot leaves that vector out
  *             (padding), one >= rows is left out and sets TQ_STATUS_RANGE; two
  *             vectors of one call must not share a row
- *   kcodes, kscales, vcodes, vscales   dev out, the cache arrays (`rows` rows);
- *             rows that no slot names keep their contents
+ *   kcodes, kscales, vcodes, vscales   dev out, the cache arrays (`rows` rows; may
+ *             be NULL for 0); rows that no slot names keep their contents
  * n * Hkv < 2^31 (TQ_EUNSUPPORTED otherwise).
  * Errors: TQ_EINVAL, TQ_EUNSUPPORTED, TQ_EALIGN, TQ_ECUDA.
  */

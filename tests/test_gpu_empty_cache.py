@@ -1,5 +1,5 @@
-"""A cache of no rows, whose arrays have no address: every page id lies
-outside it."""
+"""A cache of no rows, whose arrays have no address: every slot and every page id
+lies outside it."""
 import math
 
 import pytest
@@ -33,3 +33,23 @@ def test_fewer_rows_than_a_page():
     c.run()
     assert (c.out == 0).all() and (c.lse == -math.inf).all()
     assert tq.tq_device_status(c.h) == tq.TQ_STATUS_RANGE
+
+
+def test_writes_are_left_out_and_reads_give_zeros():
+    d = 64
+    h = tq.tq_create_kv8(d)
+    k = torch.randn(3, 2, d, device=DEV)
+    cache = no_rows(d)
+    slots = torch.full((3, 2), -1, device=DEV)
+    tq.tq_quant_kv8(h, k, k, slots, *cache)
+    assert tq.tq_device_status(h) == 0                        # padding is no event
+    slots[1, 0] = 0
+    tq.tq_quant_kv8(h, k, k, slots, *cache)
+    assert tq.tq_device_status(h) == tq.TQ_STATUS_RANGE
+    ko, vo = torch.full((6, d), 7.0, device=DEV), torch.full((6, d), 7.0, device=DEV)
+    tq.tq_dequant_kv8(h, slots, *cache, ko, vo)
+    assert (ko == 0).all() and (vo == 0).all()
+    assert tq.tq_device_status(h) == tq.TQ_STATUS_RANGE
+    tq.tq_quant_kv8(h, k, None, slots, *cache[:2])
+    tq.tq_dequant_kv8(h, slots, *cache[:2], None, None, ko)
+    assert (ko == 0).all() and tq.tq_device_status(h) == tq.TQ_STATUS_RANGE
