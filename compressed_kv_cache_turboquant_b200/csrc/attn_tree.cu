@@ -10,7 +10,7 @@
 // as fp16 (bf16 ones with a power of two per row: their 8 bits fit; what falls
 // below fp16's range is under 2^-40 of the row's largest), the weights p s' as
 // bf16, whose range holds whatever the scales are, in two terms: rounded once, few
-// keys under a row cost 2^-9 beside the result's own rounding (measured on 1000
+// keys under a row cost 2^-8 beside the result's own rounding (measured on 1000
 // keys: 0.0028 of the result, 0.0016 with the remainder's product, the plain
 // formula in 64 bits rounded to bf16).  Up to 8 rows the remainders are the other
 // half of the 16-row fragment and cost nothing; for 9 to 32 rows they are a second
@@ -32,8 +32,11 @@
 //
 // What bounds it: turning codes into 16-bit pairs and the softmax keep half of the
 // issue slots busy; the rest is their latency, with 15 warps an SM.  One token for 8
-// sequences of 131072, 8 kv-heads, 4 rows each, pages of 64: 0.489 ms, 4530 GB/s of
-// 6560.
+// sequences of 131072, 8 kv-heads, 4 rows each, pages of 64: 0.529 ms, 4190 GB/s of
+// 6560 (0.489 in a loop of nothing but this call over two caches).  At d > 128 blocks
+// hold 16 rows at most, so 256 rows read and convert the context 16 times: 64 tokens for
+// 4 sequences of 16384, d = 256: 0.97 ms (16 tokens, 64 rows: 0.28; one token for 8
+// sequences of 131071: 0.854 ms, 5100 GB/s).
 //
 // A warp beside them keeps a ring of tiles filled: one TMA load per page piece for
 // the codes (rows of 64 or 128 bytes, swizzled so that the lanes' 16-byte reads

@@ -4,7 +4,8 @@
 // The arithmetic is that of attn_tree.cu: both products run on the integer
 // codes, exact in 16 bits, with the scales on the float32 logits and on the
 // weights (rounded once to bf16; for fp16 results the remainder of that rounding
-// takes a second product).  A row is a (token, head of a kv-head's group) pair,
+// takes a second product; attn_tree.cu has it for both, so that a bf16 result of up to
+// 32 rows is off by 0.0016 of itself where this one is off by 0.0024).  A row is a (token, head of a kv-head's group) pair,
 // 128 / G tokens of a group of G heads in a tile of 128 rows, one or two tiles a
 // block; queries enter as they are.  Against attn_tree.cu's blocks of 32 rows
 // the codes of a key tile are converted once for up to 256 rows.
@@ -12,8 +13,8 @@
 // What bounds it: the softmax, which reads two scales a key (16 bytes at a time, the
 // same for all lanes) beside its 2^x, and packs the weights once, or twice with the
 // remainders.  64 tokens for 4 sequences of 16384, 8 kv-heads of 4 heads, d = 128:
-// 0.138 ms, 500 TFLOP/s; 61 tokens for 4 of 64000, 4 kv-heads, d = 64: 0.197 ms for
-// bf16 (325 TFLOP/s), 0.231 for fp16.  A second term for bf16 weights would cost a
+// 0.140 ms, 490 TFLOP/s; 61 tokens for 4 of 64000, 4 kv-heads, d = 64: 0.191 ms for
+// bf16 (335 TFLOP/s), 0.230 for fp16.  A second term for bf16 weights would cost a
 // third (0.179 ms in the first case).
 //
 // With one row tile its key tiles go to two streams in turn, each with its own

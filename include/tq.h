@@ -30,8 +30,9 @@
  *   that runs past its time limit, a shared-memory window that is not where
  *   tq_create measured it) leaves early and sets a bit in the handle's device
  *   status word; the call has already returned TQ_OK by then, and that call's
- *   outputs are incomplete.  Callers that must know poll tq_device_status
- *   after their stream has reached the calls in question.
+ *   outputs are incomplete.  A call over the 8-bit cache that leaves out a place
+ *   outside its arrays sets a bit too, and completes.  Callers that must know
+ *   poll tq_device_status.
  *
  * Packed code layout (the pages say only that 32-bit coordinates become 2- or
  * 4-bit integers, [ttakun, "为什么随机旋转是整个算法的底层杠杆"]).  A vector's d rotated
@@ -383,7 +384,7 @@ TQ_API size_t tq_attn_prefill_workspace(tq_handle hk, int B, int nq, int Hq, int
  * token all of whose logits are -infinity gives out = 0 and lse = -infinity.
  * Sums are float32 and run before the division: values above 2^90 may overflow.
  * The softmax weights enter the value product rounded to `dtype`; a float16 one
- * is off by 2^-12 of itself or 2^-32 of the row's largest weight, whichever is more.
+ * is off by 2^-11 of itself or 2^-32 of the row's largest weight, whichever is more.
  * Supported: Hq / Hkv <= 128, nseq <= TQ_MAX_SEQS, total <= 2^31 / 128.
  * Errors: TQ_EINVAL, TQ_EUNSUPPORTED, TQ_EALIGN, TQ_EWORKSPACE, TQ_ECUDA.
  */
@@ -496,8 +497,12 @@ TQ_API int tq_attn_decode_paged(tq_handle hk, tq_handle hv, const void* q, int q
 
 /*
  * The 8-bit cache holds tokens that are too new or too short-lived for a
- * rotation and a codebook (the newest window, drafted tokens, layers kept at
- * higher precision) beside a TurboQuant cache, in the same rows and pages
+ * rotation and a codebook (young sequences, drafted tokens, layers kept at
+ * higher precision), in rows and pages as those of a TurboQuant cache.  A
+ * sequence's layer lies in one of the two: tq_attn_tree attends to 8-bit rows
+ * only and tq_attn_decode_paged to compressed ones only, and what they return
+ * does not combine into one softmax over both; rows move on through
+ * tq_dequant_kv8 and tq_quant_paged
  * ([ttakun, "新旧量化方案深度权衡矩阵"]: each token is compressed as it arrives;
  * [tmdm, "实测数据"]: only the KV store and load change; the 8-bit form itself is
  * not on the pages).  A row (one token of one kv-head) x is kept as
@@ -543,8 +548,8 @@ TQ_API int tq_quant_kv8(tq_handle h, const void* k, const void* v, int dtype, in
  * cache through tq_quant_paged).
  *   slots     dev in, [n] int64; a negative slot gives a row of zeros, one >=
  *             rows too, and sets TQ_STATUS_RANGE
- *   k, v      dev out, [n][d] of out_dtype (TQ_F32, TQ_BF16 or TQ_F16), each value
- *             rounded once; v NULL: keys only (vcodes, vscales may be NULL)
+ *   k, v      dev out, [n][d] of out_dtype (TQ_F32, TQ_BF16 or TQ_F16): the float32
+ *             product c s, rounded to out_dtype; v NULL: keys only (vcodes, vscales may be NULL)
  * n < 2^31 (TQ_EUNSUPPORTED otherwise).
  * Errors: TQ_EINVAL, TQ_EUNSUPPORTED, TQ_EALIGN, TQ_ECUDA.
  */
@@ -581,6 +586,11 @@ TQ_API int tq_dequant_kv8(tq_handle h, int64_t n, const int64_t* slots, const in
  * are negative or pass the block table, and page ids outside the cache, count
  * as absent keys and set TQ_STATUS_RANGE.  Codes and scales of keys that a token
  * does not see have no part in its result, whatever they hold.
+ * The softmax weights (a value's scale in them) enter the value product as
+ * bfloat16 with the remainder of that rounding as a second term, except for
+ * bfloat16 results of more than 32 rows (n Hq / Hkv; d and Hq / Hkv <= 128), where each is
+ * rounded once, 2^-8 of itself: a draft's results and those of the same tokens one
+ * by one may differ by that beside their own rounding.
  * Sums are float32 and run before the division: values above 2^90 may overflow.
  * Supported: n <= TQ_MAX_DRAFT, B <= TQ_MAX_SEQS, rows < 2^31 - 4096
  * (TQ_EUNSUPPORTED otherwise).
@@ -728,10 +738,11 @@ TQ_API int tq_dequant_polar(tq_handle h, const uint32_t* codes, const float* nor
 
 /*
  * tq_device_status -- read and clear the handle's device status word
- * (synchronous: waits for the device).  0 = no event.  A kernel that sets a
- * bit has left before writing all of its outputs, and the call that launched
- * it has returned TQ_OK: callers that need to know poll this word.  Bit 0 (TQ_STATUS_TIMEOUT): a tensor-core
- * kernel gave up a wait on one of its own pipeline barriers after ~2 s and
+ * (synchronous: waits for all work on the handle's device).  0 = no event.  A
+ * kernel that sets bit 0 or 1 has left before writing all of its outputs, one
+ * that sets bit 2 has written them, and the call that launched it has returned
+ * TQ_OK: callers that need to know poll this word.  Bit 0 (TQ_STATUS_TIMEOUT): a
+ * tensor-core kernel gave up a wait on one of its own pipeline barriers after ~2 s and
  * returned early; its outputs for that call are incomplete.  Bit 1
  * (TQ_STATUS_LAYOUT): a decode or logits kernel built for the shared-memory
  * address that tq_create measured found its dynamic shared window elsewhere
