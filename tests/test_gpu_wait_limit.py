@@ -3,6 +3,7 @@ time.  A kernel of one warp, built here from the library's own header, waits on 
 barrier that nothing completes; it returns by itself and reports how long it took."""
 import ctypes
 import os
+import shutil
 import subprocess
 
 import pytest
@@ -45,7 +46,9 @@ extern "C" int run(int which, unsigned long long* host) {
 def test_a_wait_that_nothing_ends_gives_up_after_two_seconds(root, tmp_path):
     src, lib = tmp_path / "wait.cu", tmp_path / "wait.so"
     src.write_text(SOURCE)
-    nvcc = os.environ.get("NVCC") or "/usr/local/cuda/bin/nvcc"
+    nvcc = os.environ.get("NVCC") or shutil.which("nvcc") or shutil.which("/usr/local/cuda/bin/nvcc")
+    if not nvcc:
+        pytest.skip("needs nvcc")
     subprocess.run([nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-std=c++17", "-O3", "-shared", "-Xcompiler", "-fPIC",
                     "-I", os.path.join(root, "compressed_kv_cache_turboquant_b200", "csrc"), "-I", os.path.join(root, "include"),
                     str(src), "-o", str(lib)], check=True)
